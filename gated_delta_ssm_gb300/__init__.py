@@ -24,6 +24,7 @@ __all__ = [
     "recurrence_scan",
     "layer_scan", "verify_kn", "verify_commit_kn", "decode_step_bf16_state", "check_device",
     "version",
+    "AttnDims", "KvCache", "Rope", "attn_append", "attn_decode", "attn_prefill", "attn_workspace_bytes",
 ]
 
 _PKG = _os.path.dirname(_os.path.abspath(__file__))
@@ -95,6 +96,96 @@ class Params:
                         _dev(self.norm_w, "params.norm_w", _F32), self.l2_eps, self.rms_eps)
 
 
+class _CAttnDims(_ct.Structure):
+    _fields_ = [(n, _ct.c_int32) for n in ("n_seq", "n_q_heads", "n_kv_heads", "head_dim", "page_size",
+                                           "n_pages", "max_pages", "n_tokens", "max_q", "reserved")]
+
+
+class _CKvCache(_ct.Structure):
+    _fields_ = [(n, _ct.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "page_table")]
+
+
+class _CRope(_ct.Structure):
+    _fields_ = [("cos", _ct.c_void_p), ("sin", _ct.c_void_p), ("n_positions", _ct.c_int32),
+                ("rotary_dim", _ct.c_int32), ("interleaved", _ct.c_int32), ("reserved", _ct.c_int32)]
+
+
+@_dc.dataclass(frozen=True)
+class AttnDims:
+    """Shape of an attention call (see gdn_attn_dims in include/gdn.h)."""
+    n_seq: int
+    n_q_heads: int
+    n_kv_heads: int
+    n_pages: int
+    max_pages: int
+    n_tokens: int
+    max_q: int = 1
+    head_dim: int = 128
+    page_size: int = 64
+
+    def __post_init__(self):
+        object.__setattr__(self, "_c", _CAttnDims(
+            self.n_seq, self.n_q_heads, self.n_kv_heads, self.head_dim, self.page_size, self.n_pages,
+            self.max_pages, self.n_tokens, self.max_q, 0))
+        object.__setattr__(self, "_ref", _ct.byref(self._c))
+
+
+class KvCache:
+    """A paged key/value cache (see gdn_kv_cache in include/gdn.h): codes k and v
+    [n_pages][n_kv_heads][page_size][128] (float8_e4m3fn, or uint8), scales [n_pages][n_kv_heads]
+    float32, page_table [n_seq][max_pages] int32. Made once and kept: the tensors are checked here
+    and the handle holds on to them."""
+
+    def __init__(self, k, v, k_scale, v_scale, page_table):
+        code = ("float8_e4m3fn", "uint8")
+        self._c = _CKvCache(_dev(k, "cache.k", code), _dev(v, "cache.v", code),
+                            _dev(k_scale, "cache.k_scale", _F32), _dev(v_scale, "cache.v_scale", _F32),
+                            _dev(page_table, "cache.page_table", _I32))
+        self.k, self.v, self.k_scale, self.v_scale, self.page_table = k, v, k_scale, v_scale, page_table
+        self._shape = None
+        if not any(isinstance(t, int) for t in (k, v, k_scale, v_scale, page_table)):
+            if k.dim() != 4 or v.shape != k.shape:
+                raise ValueError("cache.k, cache.v: expected two [n_pages][n_kv_heads][page_size][head_dim] tensors")
+            if tuple(k_scale.shape) != tuple(k.shape[:2]) or k_scale.shape != v_scale.shape:
+                raise ValueError("cache.k_scale, cache.v_scale: expected [n_pages][n_kv_heads]")
+            if page_table.dim() != 2:
+                raise ValueError("cache.page_table: expected [n_seq][max_pages]")
+            self._shape = (*k.shape, *page_table.shape)
+        self._ref = _ct.byref(self._c)
+        self._fits = None
+
+    def _for(self, dims: AttnDims):
+        """The C struct, once the tensors are known to be of the sizes in dims."""
+        if self._fits is not dims:
+            want = (dims.n_pages, dims.n_kv_heads, dims.page_size, dims.head_dim, dims.n_seq, dims.max_pages)
+            if self._shape is not None and self._shape != want:
+                raise ValueError(f"cache: sizes {self._shape}, dims say {want} "
+                                 "(n_pages, n_kv_heads, page_size, head_dim, n_seq, max_pages)")
+            self._fits = dims
+        return self._ref
+
+
+class Rope:
+    """Position rotation table (see gdn_rope): cos and sin [n_positions][rotary_dim / 2] float32."""
+
+    def __init__(self, cos, sin, interleaved: bool = False):
+        if cos.dim() != 2 or cos.shape != sin.shape:
+            raise ValueError("rope: expected cos and sin of one shape [n_positions][rotary_dim / 2]")
+        self.cos, self.sin, self.interleaved = cos, sin, bool(interleaved)
+        self._c = _CRope(_dev(cos, "rope.cos", _F32), _dev(sin, "rope.sin", _F32), cos.shape[0],
+                         2 * cos.shape[1], int(self.interleaved), 0)
+        self._ref = _ct.byref(self._c)
+
+    @classmethod
+    def table(cls, n_positions: int, rotary_dim: int, base: float = 10000.0, interleaved: bool = False,
+              device="cuda"):
+        """The usual angles p * base^(-2 i / rotary_dim), computed in 64 bits."""
+        import torch
+        i = torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device)
+        a = torch.arange(n_positions, dtype=torch.float64, device=device)[:, None] * base ** (-i / rotary_dim)
+        return cls(a.cos().float(), a.sin().float(), interleaved)
+
+
 def library_path() -> str:
     return _LIB_PATH
 
@@ -129,6 +220,11 @@ def load():
             "gdn_verify_kn": [vp, vp, vp, vp, vp, vp, vp, vp, _ct.c_int, pp, vp, pd, i32, vp],
             "gdn_verify_commit_kn": [vp, vp, vp, vp, vp, pd, i32, vp],
         }
+        pa, pk = _ct.POINTER(_CAttnDims), _ct.POINTER(_CKvCache)
+        attend = [vp, i64, pk, vp, vp, vp, pa, f32, f32, i32, vp, _ct.c_size_t, vp]
+        sigs["gdn_attn_append"] = [vp, i64, vp, i64, vp, i64, _ct.c_int, pk, vp, vp, _ct.POINTER(_CRope), vp,
+                                   pa, vp]
+        sigs["gdn_attn_decode"] = sigs["gdn_attn_prefill"] = attend
         for name, args in sigs.items():
             fn = getattr(L, name)
             fn.argtypes = args
@@ -138,6 +234,8 @@ def load():
             getattr(L, name).argtypes = []
         L.gdn_prefill_workspace_bytes.restype = _ct.c_size_t
         L.gdn_prefill_workspace_bytes.argtypes = [pd, i32, i32]
+        L.gdn_attn_workspace_bytes.restype = _ct.c_size_t
+        L.gdn_attn_workspace_bytes.argtypes = [pa, i32]
         L.gdn_testing_set_first_wait_ns.restype = None
         L.gdn_testing_set_first_wait_ns.argtypes = [_ct.c_uint64]
         L.gdn_testing_row_splits.restype = None
@@ -426,3 +524,93 @@ def verify_commit_kn(state, conv_state, state_snap, conv_snap, n_accept, dims: D
                                        _dev(n_accept, "n_accept", _I32), _ct.byref(cd), n_draft,
                                        _stream(stream)),
            "gdn_verify_commit_kn")
+
+
+# ------------------------------------------------------------------ attention over the paged cache
+def _rows(t, name: str, dtypes, n_tokens: int, heads: int, dense: bool = False) -> tuple:
+    """(address, row stride in elements) of a [n_tokens][heads][128] or [n_tokens][heads * 128] tensor
+    whose rows may be farther apart than they are long. An int is a raw device address of dense rows."""
+    if t is None or isinstance(t, int):
+        return t, heads * 128
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
+    if t.dtype not in _torch_dtypes(*dtypes):
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(dtypes)}")
+    shape, stride = t.shape, t.stride()
+    if tuple(shape) not in ((n_tokens, heads, 128), (n_tokens, heads * 128)):
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected ({n_tokens}, {heads}, 128)")
+    if stride[-1] != 1 or (len(shape) == 3 and heads > 1 and stride[1] != 128):
+        raise ValueError(f"{name}: elements of a row must be contiguous")
+    row = stride[0] if n_tokens > 1 else heads * 128
+    if dense and row != heads * 128:
+        raise ValueError(f"{name}: rows must be dense")
+    _on_device(t, name)
+    return t.data_ptr(), row
+
+
+def _on_device(t, name: str):
+    import torch
+    if not t.is_cuda:
+        raise ValueError(f"{name}: tensor is on {t.device}, not on a CUDA device")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: tensor is on {t.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _counts(t, name: str, n: int) -> int | None:
+    if t is not None and not isinstance(t, int) and t.numel() != n:
+        raise ValueError(f"{name}: {t.numel()} entries, expected {n}")
+    return _dev(t, name, _I32)
+
+
+def attn_append(q, k, v, cache: KvCache, q_start, kv_len, rope: Rope, q_out, dims: AttnDims, stream=None):
+    """Rotate q into q_out, and rotate, quantise and append k and v; see gdn_attn_append. q and q_out
+    may both be None."""
+    n = dims.n_tokens
+    kp, ks = _rows(k, "k", _ACT, n, dims.n_kv_heads)
+    vp, vs = _rows(v, "v", _ACT, n, dims.n_kv_heads)
+    qp, qs = _rows(q, "q", _ACT, n, dims.n_q_heads)
+    op, _ = _rows(q_out, "q_out", ("bfloat16",), n, dims.n_q_heads, dense=True)
+    for t, nm in ((v, "v"), (q, "q")):
+        if t is not None and t.dtype != k.dtype:
+            raise TypeError(f"{nm}: dtype {t.dtype}, k is {k.dtype}")
+    _check(load().gdn_attn_append(qp, qs, kp, ks, vp, vs, _dtype(k), cache._for(dims),
+                                  _counts(q_start, "q_start", dims.n_seq + 1),
+                                  _counts(kv_len, "kv_len", dims.n_seq), rope._ref, op, dims._ref,
+                                  _stream(stream)),
+           "gdn_attn_append")
+
+
+def attn_workspace_bytes(dims: AttnDims, prefill: bool = False) -> int:
+    """Bytes of device workspace gdn_attn_decode (or gdn_attn_prefill) needs (0 for invalid dims)."""
+    return int(load().gdn_attn_workspace_bytes(dims._ref, int(prefill)))
+
+
+def _attend(fn: str, q, cache, q_start, kv_len, out, dims, scale, softcap, window, workspace, stream):
+    qp, qs = _rows(q, "q", ("bfloat16",), dims.n_tokens, dims.n_q_heads)
+    op, _ = _rows(out, "out", ("bfloat16",), dims.n_tokens, dims.n_q_heads, dense=True)
+    if workspace is None:
+        import torch
+        nbytes = attn_workspace_bytes(dims, fn == "gdn_attn_prefill")
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+    _check(getattr(load(), fn)(qp, qs, cache._for(dims), _counts(q_start, "q_start", dims.n_seq + 1),
+                               _counts(kv_len, "kv_len", dims.n_seq), op, dims._ref,
+                               128 ** -0.5 if scale is None else scale, softcap, window, _ptr(workspace),
+                               workspace.numel() * workspace.element_size(), _stream(stream)),
+           fn)
+
+
+def attn_decode(q, cache: KvCache, q_start, kv_len, out, dims: AttnDims, scale: float | None = None,
+                softcap: float = 0.0, window: int = 0, workspace=None, stream=None):
+    """Attention of a few tokens per sequence over the cache; see gdn_attn_decode. scale: 1/sqrt(128)
+    unless given. workspace: a device tensor of attn_workspace_bytes(dims) bytes; when None, one is
+    allocated with torch for this call."""
+    _attend("gdn_attn_decode", q, cache, q_start, kv_len, out, dims, scale, softcap, window, workspace, stream)
+
+
+def attn_prefill(q, cache: KvCache, q_start, kv_len, out, dims: AttnDims, scale: float | None = None,
+                 softcap: float = 0.0, window: int = 0, workspace=None, stream=None):
+    """Attention of many tokens per sequence over the cache; see gdn_attn_prefill. workspace:
+    attn_workspace_bytes(dims, prefill=True) bytes, or None."""
+    _attend("gdn_attn_prefill", q, cache, q_start, kv_len, out, dims, scale, softcap, window, workspace, stream)

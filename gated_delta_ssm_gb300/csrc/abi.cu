@@ -2,6 +2,7 @@
 // host-side argument validation, then one launch on the caller's stream.
 // Nothing here allocates, synchronises or keeps state between calls, beyond
 // the thread-local last-error text and a per-device cache of the SM count.
+#include <math.h>
 #include <stdio.h>
 #include <string.h>
 
@@ -10,6 +11,7 @@
 
 #include "../../include/gdn.h"
 #include "../../include/gdn_testing.h"
+#include "attn.h"
 #include "gdn_device.cuh"
 #include "gdn_kernels.h"
 
@@ -214,6 +216,90 @@ bool overlaps(const void *p, size_t pb, const void *q, size_t qb)
 {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p), c = reinterpret_cast<uintptr_t>(q);
     return a < c + qb && c < a + pb;
+}
+
+// Checks of the attention calls' dimensions.
+gdn_status check_attn_dims(const gdn_attn_dims *d)
+{
+    if (!d || d->reserved != 0 || d->n_seq < 1 || d->n_seq > 65535 || d->n_kv_heads < 1 ||
+        d->n_q_heads < 1 || d->n_q_heads % d->n_kv_heads != 0 || d->n_q_heads > (1 << 16) ||
+        d->n_pages < 1 || d->max_pages < 1 || d->n_tokens < 1 || d->max_q < 1 || d->max_q > (1 << 30) ||
+        d->head_dim < 1 || d->page_size < 1)
+        return GDN_ERR_INVALID_ARG;
+    if (d->head_dim != gdn::kD || d->n_q_heads / d->n_kv_heads > gdn::attn::kMaxGroup ||
+        (d->page_size != 16 && d->page_size != 32 && d->page_size != 64 && d->page_size != 128))
+        return GDN_ERR_UNSUPPORTED;
+    // positions are 32-bit
+    return (int64_t)d->max_pages * d->page_size > (1 << 30) ? GDN_ERR_INVALID_ARG : GDN_OK;
+}
+
+// Checks of the cache and the batch description, and their copy for the kernels.
+gdn_status attn_batch(const gdn_kv_cache *cache, const int32_t *q_start, const int32_t *kv_len,
+                      const gdn_attn_dims *d, gdn::attn::Batch &b)
+{
+    const gdn_status st = check_attn_dims(d);
+    if (st != GDN_OK)
+        return st;
+    if (!cache || !cache->k || !cache->v || !cache->k_scale || !cache->v_scale || !cache->page_table ||
+        !q_start || !kv_len || !aligned(cache->k, 16) || !aligned(cache->v, 16) ||
+        !aligned(cache->k_scale, 4) || !aligned(cache->v_scale, 4) || !aligned(cache->page_table, 4) ||
+        !aligned(q_start, 4) || !aligned(kv_len, 4))
+        return GDN_ERR_INVALID_ARG;
+    b.k = static_cast<uint8_t *>(cache->k);
+    b.v = static_cast<uint8_t *>(cache->v);
+    b.k_scale = cache->k_scale;
+    b.v_scale = cache->v_scale;
+    b.page_table = cache->page_table;
+    b.q_start = q_start;
+    b.kv_len = kv_len;
+    b.n_seq = d->n_seq;
+    b.Hq = d->n_q_heads;
+    b.Hkv = d->n_kv_heads;
+    b.G = d->n_q_heads / d->n_kv_heads;
+    b.P = d->page_size;
+    b.n_pages = d->n_pages;
+    b.max_pages = d->max_pages;
+    b.n_tokens = d->n_tokens;
+    b.max_q = d->max_q < d->n_tokens ? d->max_q : d->n_tokens;
+    return GDN_OK;
+}
+
+// Rows that are read 16 bytes at a time.
+bool rows16(const void *p, int64_t stride, int64_t used, size_t es)
+{
+    return p && aligned(p, 16) && stride >= used && (stride * (int64_t)es) % 16 == 0;
+}
+
+gdn_status attention(const void *q, int64_t q_stride, const gdn_kv_cache *cache,
+                     const int32_t *q_start, const int32_t *kv_len, void *out,
+                     const gdn_attn_dims *dims, float scale, float softcap, int32_t window,
+                     void *workspace, size_t workspace_bytes, bool prefill, gdn_stream_t stream)
+{
+    gdn::attn::AttnArgs a;
+    const gdn_status st = attn_batch(cache, q_start, kv_len, dims, a.b);
+    if (st != GDN_OK)
+        return st;
+    if (!rows16(q, q_stride, (int64_t)a.b.Hq * gdn::kD, 2) || !out || !aligned(out, 16) ||
+        !(fabsf(scale) <= 3e38f) || !(softcap >= 0.0f && softcap <= 3e38f) || window < 0 || !workspace ||
+        !aligned(workspace, 16))
+        return GDN_ERR_INVALID_ARG;
+    if (!prefill && (int64_t)a.b.G * a.b.max_q > gdn::attn::kMaxDecodeRows)
+        return GDN_ERR_UNSUPPORTED;
+    a.sm_count = gdn::sm_count();
+    const size_t need = prefill ? gdn::attn::prefill_workspace_bytes(a.sm_count)
+                                : gdn::attn::decode_workspace_bytes(a.b.G * a.b.max_q, a.sm_count);
+    if (workspace_bytes < need)
+        return GDN_ERR_INVALID_ARG;
+    a.q = q;
+    a.q_stride = q_stride;
+    a.out = out;
+    a.scale = scale;
+    a.softcap = softcap;
+    a.window = window;
+    a.ws = static_cast<uint8_t *>(workspace);
+    a.wait_ns = gdn::kDefaultWaitNs;
+    return from_cuda(prefill ? gdn::attn::launch_prefill(a, as_cuda(stream))
+                             : gdn::attn::launch_decode(a, as_cuda(stream)));
 }
 
 }  // namespace
@@ -577,6 +663,73 @@ gdn_status gdn_prefill_chunked_noalloc(float *state, float *conv_state, const vo
                                dims, n_tokens, chunk, scratch, kStaticScratchBytes, stream);
 }
 
+gdn_status gdn_attn_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                           const void *v, int64_t v_stride, gdn_dtype act_dtype,
+                           const gdn_kv_cache *cache, const int32_t *q_start,
+                           const int32_t *kv_len, const gdn_rope *rope, void *q_out,
+                           const gdn_attn_dims *dims, gdn_stream_t stream)
+{
+    gdn::attn::AppendArgs a;
+    const gdn_status st = attn_batch(cache, q_start, kv_len, dims, a.b);
+    if (st != GDN_OK)
+        return st;
+    if (!valid_dtype(act_dtype) || !rope || rope->reserved != 0 || rope->n_positions < 0 ||
+        rope->rotary_dim < 0 || rope->rotary_dim > gdn::kD || (rope->interleaved & ~1) != 0)
+        return GDN_ERR_INVALID_ARG;
+    if (rope->rotary_dim > 0 && (!rope->cos || !rope->sin || !aligned(rope->cos, 16) || !aligned(rope->sin, 16)))
+        return GDN_ERR_INVALID_ARG;
+    const size_t es = act_size(act_dtype);
+    const int64_t kv = (int64_t)a.b.Hkv * gdn::kD;
+    if (!rows16(k, k_stride, kv, es) || !rows16(v, v_stride, kv, es) || (q == nullptr) != (q_out == nullptr) ||
+        (q && (!rows16(q, q_stride, (int64_t)a.b.Hq * gdn::kD, es) || !aligned(q_out, 16))))
+        return GDN_ERR_INVALID_ARG;
+    if (rope->rotary_dim % 16 != 0)
+        return GDN_ERR_UNSUPPORTED;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.cos = rope->cos;
+    a.sin = rope->sin;
+    a.n_positions = rope->n_positions;
+    a.rot = rope->rotary_dim;
+    a.interleaved = rope->interleaved;
+    a.q_out = q_out;
+    return from_cuda(gdn::attn::launch_append(a, act_dtype == GDN_BF16, as_cuda(stream)));
+}
+
+size_t gdn_attn_workspace_bytes(const gdn_attn_dims *dims, int32_t prefill)
+{
+    if (check_attn_dims(dims) != GDN_OK)
+        return 0;
+    const int max_q = dims->max_q < dims->n_tokens ? dims->max_q : dims->n_tokens;
+    const int64_t rows = (int64_t)(dims->n_q_heads / dims->n_kv_heads) * max_q;
+    if (!prefill && rows > gdn::attn::kMaxDecodeRows)
+        return 0;
+    return prefill ? gdn::attn::prefill_workspace_bytes(gdn::sm_count())
+                   : gdn::attn::decode_workspace_bytes((int)rows, gdn::sm_count());
+}
+
+gdn_status gdn_attn_decode(const void *q, int64_t q_stride, const gdn_kv_cache *cache,
+                           const int32_t *q_start, const int32_t *kv_len, void *out,
+                           const gdn_attn_dims *dims, float scale, float softcap, int32_t window,
+                           void *workspace, size_t workspace_bytes, gdn_stream_t stream)
+{
+    return attention(q, q_stride, cache, q_start, kv_len, out, dims, scale, softcap, window, workspace,
+                     workspace_bytes, false, stream);
+}
+
+gdn_status gdn_attn_prefill(const void *q, int64_t q_stride, const gdn_kv_cache *cache,
+                            const int32_t *q_start, const int32_t *kv_len, void *out,
+                            const gdn_attn_dims *dims, float scale, float softcap, int32_t window,
+                            void *workspace, size_t workspace_bytes, gdn_stream_t stream)
+{
+    return attention(q, q_stride, cache, q_start, kv_len, out, dims, scale, softcap, window, workspace,
+                     workspace_bytes, true, stream);
+}
+
 void gdn_testing_set_first_wait_ns(uint64_t ns)
 {
     gdn::g_first_wait_ns.store(ns, std::memory_order_relaxed);
@@ -591,7 +744,7 @@ void gdn_testing_row_splits(int32_t n_seq, int32_t n_v_heads, int32_t r, int32_t
 
 gdn_status gdn_check_device(int32_t *code)
 {
-    int a = 0, b = 0, c = 0, d = 0;
+    int a = 0, b = 0, c = 0, d = 0, e = 0, f = 0, g = 0;
     gdn_status st = from_cuda(gdn::take_decode_device_error(&a));
     if (st == GDN_OK)
         st = from_cuda(gdn::take_prefill_device_error(&b));
@@ -599,7 +752,13 @@ gdn_status gdn_check_device(int32_t *code)
         st = from_cuda(gdn::take_sequential_device_error(&c));
     if (st == GDN_OK)
         st = from_cuda(gdn::take_conv_device_error(&d));
-    const int all = a | b | c | d;
+    if (st == GDN_OK)
+        st = from_cuda(gdn::attn::take_append_error(&e));
+    if (st == GDN_OK)
+        st = from_cuda(gdn::attn::take_decode_error(&f));
+    if (st == GDN_OK)
+        st = from_cuda(gdn::attn::take_prefill_error(&g));
+    const int all = a | b | c | d | e | f | g;
     if (code)
         *code = all;
     if (st != GDN_OK)

@@ -421,6 +421,149 @@ gdn_status gdn_prefill_chunked_noalloc(float *state, float *conv_state, const vo
                                        const gdn_dims *dims, int32_t n_tokens, int32_t chunk,
                                        gdn_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Softmax attention over a paged 8-bit key/value cache: the attention layers
+ * that a hybrid model interleaves with gated-delta layers. One call appends a
+ * batch's keys and values (with the position rotation applied on the way),
+ * two read the cache: gdn_attn_decode for one to a few tokens per sequence
+ * (single-token steps, draft verification) and gdn_attn_prefill for many.
+ *
+ * CACHE (gdn_kv_cache)
+ *   Keys and values are held as e4m3 codes in pages of page_size tokens, with
+ *   one float32 scale per page and KV head; the held value is code * scale.
+ *   Scales are powers of two, at least 2^-100, so a scale that grows moves the
+ *   codes already in the page exactly (but for values that fall below e4m3's
+ *   smallest step, 2^-9 of the new scale, which round to nearest even).
+ *     k, v              e4m3 [n_pages][Hkv][page_size][128]
+ *     k_scale, v_scale  float [n_pages][Hkv]
+ *     page_table        int32 [n_seq][max_pages]: page of tokens
+ *                       [i * page_size, (i + 1) * page_size) of sequence b
+ *   New pages need no initialisation: the append that writes a page's first
+ *   slot starts its scale afresh, and slots past a sequence's length are never
+ *   used, whatever they hold.
+ *
+ * BATCH
+ *   q_start int32 [n_seq + 1]: sequence b owns token rows
+ *           q_start[b] .. q_start[b + 1] - 1 of q, k, v and out (n of them, at
+ *           most max_q; the last entry at most n_tokens)
+ *   kv_len  int32 [n_seq]: tokens in the sequence's cache once this call's own
+ *           are in it. Row i of n is at position p = kv_len[b] - n + i. A row
+ *           with p < 0 is padding (e.g. an idle slot of a fixed-size batch,
+ *           kv_len 0): it is not appended, its rotated q is taken at position
+ *           0, and its attention output is zero.
+ *   These arrays live on the device and are checked by the kernels: a
+ *   sequence whose entries are out of range, or a page-table entry outside
+ *   0 .. n_pages - 1, sets bit 256 of the device error word
+ *   (gdn_check_device). Such a sequence is skipped (its outputs are not
+ *   written); tokens of such a page are not appended, and not seen.
+ *
+ * DRAFTS  To drop rejected draft tokens, lower kv_len in the next call; the
+ *   next append overwrites their slots. The page keeps the scale that they may
+ *   have raised.
+ *
+ * SUPPORTED  head_dim 128; page_size 16, 32, 64 or 128; Hq a multiple of Hkv,
+ *   G = Hq / Hkv at most 16.
+ */
+typedef struct gdn_attn_dims {
+    int32_t n_seq;        /* >= 1, <= 65535 */
+    int32_t n_q_heads;    /* Hq, a multiple of Hkv */
+    int32_t n_kv_heads;   /* Hkv >= 1 */
+    int32_t head_dim;     /* 128 */
+    int32_t page_size;    /* P */
+    int32_t n_pages;      /* pages of the cache, >= 1 */
+    int32_t max_pages;    /* columns of page_table, >= 1 */
+    int32_t n_tokens;     /* token rows of q, k, v and out, >= 1 */
+    int32_t max_q;        /* at least the most tokens any sequence has in this call */
+    int32_t reserved;     /* must be 0 */
+} gdn_attn_dims;
+
+typedef struct gdn_kv_cache {
+    void *k;              /* e4m3 codes, 16-byte aligned */
+    void *v;
+    float *k_scale;
+    float *v_scale;
+    const int32_t *page_table;
+} gdn_kv_cache;
+
+/* Position rotation: row p of cos and sin holds the rotary_dim / 2 angles of
+ * position p. The pair (a, b) becomes (a cos - b sin, b cos + a sin); pairs are
+ * (i, i + rotary_dim / 2), or (2 i, 2 i + 1) when interleaved is 1. Elements
+ * past rotary_dim are left as they are; rotary_dim 0 rotates nothing. */
+typedef struct gdn_rope {
+    const float *cos;     /* [n_positions][rotary_dim / 2] */
+    const float *sin;
+    int32_t n_positions;  /* every position of a call must be below it */
+    int32_t rotary_dim;   /* a multiple of 16, <= 128 */
+    int32_t interleaved;  /* 0 or 1 */
+    int32_t reserved;     /* must be 0 */
+} gdn_rope;
+
+/*
+ * Append a batch's keys and values to the cache, with the rotation applied to
+ * keys (and to q, into q_out) on the way; one launch.
+ *   q, k, v  act rows q_stride / k_stride / v_stride elements apart, the first
+ *            Hq*128 (Hkv*128) of a row used: rows of separate arrays or of one
+ *            fused projection. Aligned to 16 bytes, strides whole multiples of
+ *            16 bytes.
+ *   q_out    bf16 [n_tokens][Hq][128] dense: the rotated q, rounded to nearest
+ *            even. q and q_out may both be NULL (keys and values alone).
+ * Per page and KV head: the scale becomes the larger of what it was (unless
+ * this call writes the page's slot 0) and the smallest power of two s with
+ * max |new value| <= 448 s; when it grows, the page's other codes move to it;
+ * new codes are value / s rounded to nearest even. An infinite key or value is
+ * held as +-448 s and a NaN as 0 (neither counts for s), and either sets bit
+ * 512 of the device error word, so that one bad row cannot poison a page.
+ * Sequences that share a page may not append to it in one call.
+ * Errors: INVALID_ARG (null, sizes, strides, alignment, one of q and q_out
+ * NULL), UNSUPPORTED (head_dim, page_size, G, rotary_dim).
+ */
+gdn_status gdn_attn_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                           const void *v, int64_t v_stride, gdn_dtype act_dtype,
+                           const gdn_kv_cache *cache, const int32_t *q_start,
+                           const int32_t *kv_len, const gdn_rope *rope, void *q_out,
+                           const gdn_attn_dims *dims, gdn_stream_t stream);
+
+/*
+ * Workspace bytes of gdn_attn_decode (prefill = 0) or gdn_attn_prefill
+ * (prefill = 1); it depends on the heads and on max_q, not on the lengths.
+ * Returns 0 for invalid or unsupported dims.
+ */
+size_t gdn_attn_workspace_bytes(const gdn_attn_dims *dims, int32_t prefill);
+
+/*
+ * Attention of a few tokens per sequence (G * max_q <= 64) over the cache:
+ * per row at position p and head h, with the keys j of KV head h / G,
+ *   s_j = scale * (q . k_j);  s_j = softcap * tanh(s_j / softcap) if softcap > 0;
+ *   seen: j <= p, j < kv_len, and j > p - window if window > 0;
+ *   out = sum_seen e^(s_j - max s) v_j / sum_seen e^(s_j - max s).
+ * A row that sees nothing (padding) gives zeros.
+ *   q    bf16 rows q_stride elements apart (16-byte aligned, a multiple of 16
+ *        bytes apart), first Hq*128 used; already rotated (gdn_attn_append)
+ *   out  bf16 [n_tokens][Hq][128] dense, rounded to nearest even
+ *   workspace  device scratch of gdn_attn_workspace_bytes(dims, 0) bytes,
+ *        16-byte aligned; contents on entry do not matter. Calls that overlap
+ *        on the GPU need separate workspaces.
+ * Scores, statistics and sums are float32.
+ * Errors: INVALID_ARG (null, sizes, alignment, scale or softcap not finite,
+ * softcap or window negative, workspace too small), UNSUPPORTED (head_dim,
+ * page_size, G, G * max_q > 64).
+ */
+gdn_status gdn_attn_decode(const void *q, int64_t q_stride, const gdn_kv_cache *cache,
+                           const int32_t *q_start, const int32_t *kv_len, void *out,
+                           const gdn_attn_dims *dims, float scale, float softcap, int32_t window,
+                           void *workspace, size_t workspace_bytes, gdn_stream_t stream);
+
+/*
+ * The same attention for any number of tokens per sequence: whole prompts, or
+ * chunks of them behind tokens already in the cache. Arguments and errors as
+ * gdn_attn_decode, without the limit on max_q and with a workspace of
+ * gdn_attn_workspace_bytes(dims, 1) bytes.
+ */
+gdn_status gdn_attn_prefill(const void *q, int64_t q_stride, const gdn_kv_cache *cache,
+                            const int32_t *q_start, const int32_t *kv_len, void *out,
+                            const gdn_attn_dims *dims, float scale, float softcap, int32_t window,
+                            void *workspace, size_t workspace_bytes, gdn_stream_t stream);
+
 /*
  * Every wait inside a kernel on a bulk copy, a tensor-core operation,
  * another warp group of the same CTA or data pushed by another CTA of the
@@ -439,6 +582,10 @@ gdn_status gdn_prefill_chunked_noalloc(float *state, float *conv_state, const vo
  *   bit 128 a row slice of a fused decode / verify step gave up waiting for
  *           the gated-norm partial sums of the head's other row slices (that
  *           head's outputs are not valid)
+ *   bit 256 an attention call's q_start, kv_len or page_table held an entry out
+ *           of range, or a position past the rotation table
+ *   bit 512 gdn_attn_append met a key or value that is not finite
+ *   bit 1024 an attention kernel gave up a wait (its outputs are not valid)
  * The one wait not bounded by the library is the hardware's tensor-memory
  * allocation at the start of the prefill kernels, which lasts until CTAs of
  * other launches on the same SM release their columns. This call waits for
