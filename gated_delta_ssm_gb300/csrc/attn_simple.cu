@@ -90,12 +90,10 @@ static cudaError_t launch_simple(const AttnArgs &a, cudaStream_t s)
     return cudaGetLastError();
 }
 
-cudaError_t launch_decode(const AttnArgs &a, cudaStream_t s) { return launch_simple(a, s); }
 cudaError_t launch_prefill(const AttnArgs &a, cudaStream_t s) { return launch_simple(a, s); }
-size_t decode_workspace_bytes(int, int) { return 16; }
 size_t prefill_workspace_bytes(int) { return 16; }
 
-cudaError_t take_decode_error(int *code)
+cudaError_t take_prefill_error(int *code)
 {
     int v = 0;
     cudaError_t e = cudaMemcpyFromSymbol(&v, g_attn_error, sizeof(int));
@@ -106,11 +104,5 @@ cudaError_t take_decode_error(int *code)
     *code = v;
     return e;
 }
-cudaError_t take_prefill_error(int *code)
-{
-    *code = 0;
-    return cudaSuccess;
-}
-
 }  // namespace attn
 }  // namespace gdn
