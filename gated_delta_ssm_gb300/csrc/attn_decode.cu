@@ -37,11 +37,6 @@ static __device__ int g_attn_decode_error;
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kOwner = 1;                     // meta: this CTA's last segment begins here and goes on
-
-struct PartMeta {
-    int b, h, last_cta, flags;
-};
 
 template <int NR>
 struct Cfg {
@@ -129,19 +124,6 @@ __device__ __forceinline__ Walk walk_start(const AttnArgs &A, const S &sh, int c
     return w;
 }
 
-__device__ __forceinline__ int64_t share_begin(int64_t total, int n, int c) { return total * c / n; }
-__device__ __forceinline__ int share_of(int64_t total, int n, int64_t unit)
-{
-    return (int)(((unit + 1) * n - 1) / total);
-}
-
-__device__ __forceinline__ float redux_max(float x)
-{
-    float y;
-    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 template <int NR>
 __global__ void __launch_bounds__(kThreads, Cfg<NR>::kCtas)
 attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ CUtensorMap map_k,
@@ -176,7 +158,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sh.abort = 0;
-        sh.start_b = -1;
+        sh.start_b = 0;
     }
     if (warp == 1)
         tc::tmem_alloc(tc::smem_addr(&sh.tmem), C::kTmemCols);
@@ -231,9 +213,9 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
         }
     }
     PartMeta *const meta = reinterpret_cast<PartMeta *>(A.ws);
-    float *const parts = reinterpret_cast<float *>(A.ws + (size_t)gridDim.x * sizeof(PartMeta));
+    float *const parts = part_slots(A.ws, gridDim.x);
     if (tid == 0)
-        meta[blockIdx.x].flags = 0;
+        meta[blockIdx.x].owner = 0;
     __syncthreads();
     allow_next_grid();
 
@@ -243,7 +225,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
     // A wait that gives up stops the CTA's copies and products and ends every other wait; the loops
     // run on to their ends.
     auto wait1 = [&](const uint64_t &bar, uint32_t parity) {
-        if (!tc::mbar_wait_ns(tc::smem_addr(&bar), parity, lim, &sh.abort)) {
+        if (!wait_phase(tc::smem_addr(&bar), parity, lim, &sh.abort)) {
             sh.abort = 1;
             failed = true;
         }
@@ -388,58 +370,24 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
                 for (int r = r8; r < NR; r += 8) {
                     const int tok = r / B.G, g = r - tok * B.G;
                     const bool live = tok < w.q.s.n;
-                    float v[16];
+                    float v[16] = {};
+                    if (live)
+                        load_q16(static_cast<const __nv_bfloat16 *>(A.q) +
+                                     (int64_t)(w.q.s.row0 + tok) * A.q_stride + (w.h * B.G + g) * kHd + u * 16,
+                                 v);
                     float top = 0.0f;
-                    if (live) {
-                        const uint4 *src = reinterpret_cast<const uint4 *>(
-                            static_cast<const __nv_bfloat16 *>(A.q) + (int64_t)(w.q.s.row0 + tok) * A.q_stride +
-                            (w.h * B.G + g) * kHd + u * 16);
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const uint4 x = __ldg(src + c);
-                            const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                v[8 * c + 2 * e] = __uint_as_float(y[e] << 16);
-                                v[8 * c + 2 * e + 1] = __uint_as_float(y[e] & 0xffff0000u);
-                            }
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            v[e] = 0.0f;
-                    }
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
                         top = fmaxf(top, fabsf(v[e]));
 #pragma unroll
                     for (int m = 1; m < 8; m <<= 1)
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-                    // q 2^x: the largest magnitude lands in [128, 256)
-                    const int ex = top > 0.0f ? min(126, 134 - (int)(__float_as_uint(top) >> 23)) : 0;
-                    const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        hi[c] = lo[c] = 0;
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float a = v[4 * c + 2 * e] * up, b2 = v[4 * c + 2 * e + 1] * up;
-                            const __nv_fp8x2_storage_t h8 =
-                                __nv_cvt_float2_to_fp8x2(make_float2(a, b2), __NV_SATFINITE, __NV_E4M3);
-                            const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h8, __NV_E4M3)));
-                            const __nv_fp8x2_storage_t l8 = __nv_cvt_float2_to_fp8x2(
-                                make_float2(a - back.x, b2 - back.y), __NV_SATFINITE, __NV_E4M3);
-                            hi[c] |= (uint32_t)h8 << (16 * e);
-                            lo[c] |= (uint32_t)l8 << (16 * e);
-                        }
-                    }
-                    uint8_t *dst = mem + C::kQ + k * 2 * C::kRowBytes + (r >> 3) * 1024 + (r & 7) * 128 +
-                                   ((u ^ (r & 7)) << 4);
-                    *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(dst + C::kRowBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    const int ex = q_exponent(top);
+                    store_q16(mem + C::kQ + k * 2 * C::kRowBytes + (r >> 3) * 1024 + (r & 7) * 128 +
+                                  ((u ^ (r & 7)) << 4),
+                              C::kRowBytes, v, q_factor(top));
                     if (u == 0) {
-                        sh.f[k][r] = A.scale * kLog2e * __uint_as_float((uint32_t)(127 - ex) << 23);
+                        sh.f[k][r] = A.scale * kLog2e * pow2i(-ex);
                         sh.limit[k][r] = live ? w.q.s.L - w.q.s.n + tok : -1;
                     }
                 }
@@ -545,11 +493,8 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
                         const float p0 = ex2(x[r] - c0.x), p1 = ex2(x[r + 1] - c1.x);
                         l[r] = fmaf(l[r], c0.y, p0 * (c0.z * iv));
                         l[r + 1] = fmaf(l[r + 1], c1.y, p1 * (c1.z * iv));
-                        const __nv_fp8x2_storage_t h8 =
-                            __nv_cvt_float2_to_fp8x2(make_float2(p0, p1), __NV_SATFINITE, __NV_E4M3);
-                        const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h8, __NV_E4M3)));
-                        const __nv_fp8x2_storage_t l8 = __nv_cvt_float2_to_fp8x2(
-                            make_float2(p0 - back.x, p1 - back.y), __NV_SATFINITE, __NV_E4M3);
+                        uint32_t h8, l8;
+                        split_e4m3(p0, p1, h8, l8);
                         uint8_t *a = prow + (r >> 3) * 1024 + (r & 7) * 128 + (((t >> 4) ^ (r & 7)) << 4);
                         uint8_t *b = prow + (r >> 3) * 1024 + ((r + 1) & 7) * 128 +
                                      (((t >> 4) ^ ((r + 1) & 7)) << 4);
@@ -639,30 +584,25 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
                                         (sh.l_sum[k][2][r] + sh.l_sum[k][3][r]);
                         const int tok = r / B.G, g = r - tok * B.G;
                         out[((int64_t)tok * B.Hq + g) * kHd] =
-                            __float2bfloat16_rn(l > 0.0f ? __fdividef(o[r], l) : 0.0f);
+                            __float2bfloat16_rn(l > 0.0f ? o[r] / l : (l == l ? 0.0f : l));
                     }
                 } else {
                     const int slot = 2 * blockIdx.x + (w.begins() ? 1 : 0);
-                    float *dst = parts + (size_t)slot * R * (kHd + 4);
+                    float *dst = parts + (size_t)slot * R * kPartRow;
 #pragma unroll
                     for (int r = 0; r < NR; ++r) {
                         if (r >= rows)
                             break;
-                        dst[r * kHd + d] = o[r];
+                        dst[r * kPartRow + d] = o[r];
                         if (d == 0) {
-                            dst[R * kHd + 4 * r] = (sh.l_sum[k][0][r] + sh.l_sum[k][1][r]) +
-                                                   (sh.l_sum[k][2][r] + sh.l_sum[k][3][r]);
-                            dst[R * kHd + 4 * r + 1] = sh.w_max[k][r];
+                            dst[r * kPartRow + kHd] = (sh.l_sum[k][0][r] + sh.l_sum[k][1][r]) +
+                                                     (sh.l_sum[k][2][r] + sh.l_sum[k][3][r]);
+                            dst[r * kPartRow + kHd + 1] = sh.w_max[k][r];
                         }
                     }
                     if (w.begins() && d == 0) {
                         const int64_t end_unit = first + count - w.left + (w.q.n - w.t);   // past its last tile
-                        PartMeta m;
-                        m.b = w.b;
-                        m.h = w.h;
-                        m.last_cta = share_of(total, n_cta, end_unit - 1);
-                        m.flags = kOwner;
-                        meta[blockIdx.x] = m;
+                        meta[blockIdx.x] = {w.b, w.h, 0, share_of(total, n_cta, end_unit - 1), 1, {}};
                     }
                 }
                 tc::mbar_arrive(tc::smem_addr(&sh.l_free[k]));
@@ -677,48 +617,6 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
     tc::fence_after_sync();
     if (warp == 1)
         tc::tmem_dealloc(tmem, C::kTmemCols);
-}
-
-// Join the partial results of a (sequence, KV head): CTA x owns the one that begins in share x. A warp
-// per row, four dimensions per lane.
-__global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnArgs A, int R)
-{
-    const Batch &B = A.b;
-    wait_previous_grid();
-    allow_next_grid();
-    const PartMeta m = reinterpret_cast<const PartMeta *>(A.ws)[blockIdx.x];
-    if (!(m.flags & kOwner))
-        return;
-    const Seq s = load_seq(B, m.b);
-    const int r = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (r >= s.n * B.G)
-        return;
-    const float *parts = reinterpret_cast<const float *>(A.ws + (size_t)gridDim.x * sizeof(PartMeta));
-    const size_t size = (size_t)R * (kHd + 4);
-    float big = -INFINITY, l = 0.0f;
-    float4 o = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-    for (int c = blockIdx.x; c <= m.last_cta; ++c) {
-        const float *p = parts + (size_t)(2 * c + (c == (int)blockIdx.x ? 1 : 0)) * size;
-        const float2 lw = *reinterpret_cast<const float2 *>(p + R * kHd + 4 * r);
-        const float4 x = *reinterpret_cast<const float4 *>(p + r * kHd + 4 * lane);
-        const float grown = fmaxf(big, lw.y);
-        if (grown == -INFINITY)
-            continue;
-        const float a = ex2(big - grown), b = ex2(lw.y - grown);
-        l = fmaf(l, a, lw.x * b);
-        o.x = fmaf(o.x, a, x.x * b);
-        o.y = fmaf(o.y, a, x.y * b);
-        o.z = fmaf(o.z, a, x.z * b);
-        o.w = fmaf(o.w, a, x.w * b);
-        big = grown;
-    }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    const int tok = r / B.G, g = r - tok * B.G;
-    __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-    uint2 w = make_uint2(*reinterpret_cast<uint32_t *>(&lo), *reinterpret_cast<uint32_t *>(&hi));
-    reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(A.out) +
-                              ((int64_t)(s.row0 + tok) * B.Hq + m.h * B.G + g) * kHd)[lane] = w;
 }
 
 int row_pad(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
@@ -746,19 +644,14 @@ cudaError_t launch_rows(const AttnArgs &a, int grid, cudaStream_t s)
     cfg.numAttrs = 1;
     if ((e = cudaLaunchKernelEx(&cfg, attn_decode_kernel<NR>, a, mk, mv)) != cudaSuccess)
         return e;
-    const int R = a.b.G * a.b.max_q;
-    cfg.gridDim = dim3(grid, (R + 3) / 4);
-    cfg.blockDim = dim3(128);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel, a, R);
+    return launch_join(a, grid, a.b.G * a.b.max_q, s);
 }
 
 }  // namespace
 
 size_t decode_workspace_bytes(int rows, int sms)
 {
-    const size_t ctas = (size_t)most_ctas(rows, sms);
-    return ctas * (sizeof(PartMeta) + 2 * (size_t)rows * (kHd + 4) * sizeof(float));
+    return part_bytes((size_t)most_ctas(rows, sms), (size_t)rows);
 }
 
 cudaError_t launch_decode(const AttnArgs &args, cudaStream_t s)

@@ -30,5 +30,24 @@ __device__ __forceinline__ Seq load_seq(const Batch &B, int b)
     return s;
 }
 
+// ------------------------------------------------------------------ partial results
+// Where a block of q rows spans several CTAs' shares, the CTA in which it begins describes it here and
+// every CTA leaves a part: [2 * grid] slots of `rows` rows, after the descriptions in the workspace.
+struct PartMeta {
+    int b, h, row0, last_cta;   // row0: the block's first row, token * G + head of the group
+    int owner, pad[3];
+};
+constexpr int kPartRow = kHd + 4;   // 128 sums, l, m, two unused
+
+__device__ __forceinline__ float *part_slots(uint8_t *ws, unsigned grid)
+{
+    return reinterpret_cast<float *>(ws + (size_t)grid * sizeof(PartMeta));
+}
+inline size_t part_bytes(size_t ctas, size_t rows)
+{
+    return ctas * (sizeof(PartMeta) + 2 * rows * kPartRow * sizeof(float));
+}
+cudaError_t launch_join(const AttnArgs &a, int grid, int rows, cudaStream_t s);
+
 }  // namespace attn
 }  // namespace gdn

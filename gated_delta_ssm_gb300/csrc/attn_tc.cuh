@@ -5,6 +5,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
+#include <math_constants.h>
 
 #include "attn_device.cuh"
 #include "tc_ptx.cuh"
@@ -41,6 +42,103 @@ __device__ __forceinline__ float ex2(float x)
 __device__ __forceinline__ void named_sync(int id, int threads)
 {
     asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
+}
+
+__device__ __forceinline__ float redux_max(float x)
+{
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The batch's tiles shared out over n CTAs: share c begins at unit total * c / n.
+__device__ __forceinline__ int64_t share_begin(int64_t total, int n, int c) { return total * c / n; }
+__device__ __forceinline__ int share_of(int64_t total, int n, int64_t unit)
+{
+    return (int)(((unit + 1) * n - 1) / total);
+}
+
+// Two e4m3 numbers whose sum is (x, y) to within 2^-8 of each, down to steps of 2^-9: the low byte of
+// each result is x's.
+__device__ __forceinline__ void split_e4m3(float x, float y, uint32_t &hi, uint32_t &lo)
+{
+    hi = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+    const float2 back =
+        __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3)));
+    lo = __nv_cvt_float2_to_fp8x2(make_float2(x - back.x, y - back.y), __NV_SATFINITE, __NV_E4M3);
+}
+
+// 16 elements of a q row (16 bytes aligned), bf16 to float.
+__device__ __forceinline__ void load_q16(const __nv_bfloat16 *p, float (&v)[16])
+{
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p) + c);
+        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[8 * c + 2 * e] = __uint_as_float(y[e] << 16);
+            v[8 * c + 2 * e + 1] = __uint_as_float(y[e] & 0xffff0000u);
+        }
+    }
+}
+
+// x with 2^x top in [128, 256) (0 for top = 0); at most 126, so that 2^x stays finite.
+__device__ __forceinline__ int q_exponent(float top)
+{
+    return top > 0.0f ? min(126, 134 - (int)(__float_as_uint(top) >> 23)) : 0;
+}
+__device__ __forceinline__ float pow2i(int x) { return __uint_as_float((uint32_t)(x + 127) << 23); }
+
+// The factor of a q row whose largest magnitude is top: 2^q_exponent, or NaN for a row that holds an
+// infinity, which makes the whole row NaN as the formula does.
+__device__ __forceinline__ float q_factor(float top)
+{
+    return top < CUDART_INF_F ? pow2i(q_exponent(top)) : CUDART_NAN_F;
+}
+
+// The 16 elements times `up` as hi + lo, at dst and dst + lo_at.
+__device__ __forceinline__ void store_q16(uint8_t *dst, uint32_t lo_at, const float (&v)[16], float up)
+{
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t h0, l0, h1, l1;
+        split_e4m3(v[4 * c] * up, v[4 * c + 1] * up, h0, l0);
+        split_e4m3(v[4 * c + 2] * up, v[4 * c + 3] * up, h1, l1);
+        hi[c] = h0 | h1 << 16;
+        lo[c] = l0 | l1 << 16;
+    }
+    *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4 *>(dst + lo_at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+}
+
+// Wait for a phase, at most limit_ns of the global timer, or until *abort. A try sleeps for as long as the
+// hardware sees fit. The timer is read once in 256 tries. A limit under 1 us gives up at once, without a
+// try: a test hook takes that path.
+__device__ __forceinline__ bool wait_phase(uint32_t mbar, uint32_t parity, uint64_t limit_ns,
+                                           const volatile int *abort)
+{
+    if (limit_ns < 1000)
+        return false;
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+        uint32_t done;
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(done) : "r"(mbar), "r"(parity) : "memory");
+        if (done)
+            return true;
+        if (*abort != 0)
+            return false;
+        if (i % 256 == 0) {
+            const uint64_t now = tc::global_ns();
+            if (t0 == 0)
+                t0 = now;
+            else if (now - t0 > limit_ns)
+                return false;
+        }
+    }
 }
 
 // One box (one page of one head: P rows of 128 bytes) into shared memory.
