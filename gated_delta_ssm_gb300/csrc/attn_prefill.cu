@@ -214,15 +214,12 @@ __device__ __forceinline__ float2 unpack2(uint64_t a)
 template <bool CAP, bool WHOLE, typename M, typename F>
 __device__ __forceinline__ float row_max(uint32_t s_at, M mask_of, F factor, float cap2, float inv_cap2)
 {
-    uint32_t x[2][32];
     float top = -INFINITY;
-    tmem_get32(s_at, x[0]);
-#pragma unroll
+#pragma unroll 1
     for (int q4 = 0; q4 < 4; ++q4) {
-        uint32_t(&v)[32] = x[q4 & 1];
+        uint32_t v[32];
+        tmem_get32(s_at + 32 * q4, v);
         tmem_wait32(v);
-        if (q4 < 3)
-            tmem_get32(s_at + 32 * (q4 + 1), x[(q4 + 1) & 1]);
         const uint32_t mask = WHOLE ? 0xffffffffu : mask_of(q4);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -249,16 +246,13 @@ template <bool CAP, bool WHOLE, typename M, typename F>
 __device__ __forceinline__ float row_weights(uint32_t s_at, M mask_of, F factor, float sub, float cap2,
                                              float inv_cap2)
 {
-    uint32_t x[2][32];
     uint64_t sum[2] = {0, 0};
     const uint64_t sub2 = pack2(-sub, -sub);
-    tmem_get32(s_at, x[0]);
-#pragma unroll
+#pragma unroll 1
     for (int q4 = 0; q4 < 4; ++q4) {
-        uint32_t(&v)[32] = x[q4 & 1];
+        uint32_t v[32];
+        tmem_get32(s_at + 32 * q4, v);
         tmem_wait32(v);
-        if (q4 < 3)
-            tmem_get32(s_at + 32 * (q4 + 1), x[(q4 + 1) & 1]);
         const uint32_t mask = WHOLE ? 0xffffffffu : mask_of(q4);
         uint32_t y[16];
 #pragma unroll
@@ -513,18 +507,18 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
             constexpr uint32_t idesc_s = idesc_e4m3(128, 128);
             constexpr uint32_t idesc_o = tc::idesc_f16(128, 128) | 1u << 7 | 1u << 10 | tc::kIdescTransB;
             Walk w = walk_start(A, sh, count);
-            int seg[2] = {0, 0};        // segment of the next scores of A, B
+            int seg_a = 0, seg_b = 0;   // segment of the next scores of A, B
             int c = 0;                  // the tile of scores: same for A and B
             int t = w.t;
             bool last_of_seg = t + 1 == w.end;
             auto scores = [&](int m) {  // S of tile c
                 const int ks = c % kKs;
-                wait1(sh.q_full[m], seg[m] & 1);
+                wait1(sh.q_full[m], (m ? seg_b : seg_a) & 1);
                 wait1(sh.k_full[ks], (c / kKs) & 1);
                 tc::fence_after_sync();
                 if (!sh.abort) {
                     const uint64_t k = tc::sdesc_sw128(base + kKAt + ks * kTileBytes);
-#pragma unroll
+#pragma unroll 1
                     for (int part = 0; part < 2; ++part) {
                         const uint64_t q = tc::sdesc_sw128(base + kQAt + (2 * m + part) * kTileBytes);
 #pragma unroll
@@ -535,7 +529,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                 tc::mma_commit(tc::smem_addr(&sh.s_full[m]));
                 if (last_of_seg) {
                     tc::mma_commit(tc::smem_addr(&sh.q_free[m]));
-                    ++seg[m];
+                    m ? ++seg_b : ++seg_a;
                 }
                 if (m == 1)
                     tc::mma_commit(tc::smem_addr(&sh.k_free[ks]));
@@ -553,7 +547,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                 if (!sh.abort) {
                     const uint64_t v =
                         tc::sdesc_sw128_mn(base + kBAt + (j % kVb) * 2 * kTileBytes, kTileBytes, 1024);
-#pragma unroll
+#pragma unroll 2
                     for (int s = 0; s < 8; ++s)   // 16 keys: 8 columns of P, 2 KB of V
                         tc::mma_f16_ta(tmem + 256 + m * 128, tmem + m * 128 + 8 * s, v + 128 * s, idesc_o,
                                        !begin || s > 0);
@@ -563,18 +557,20 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                     tc::mma_commit(tc::smem_addr(&sh.b_free[j % kVb]));
             };
             bool begin = true, begin_next = last_of_seg;
-            scores(0);
-            scores(1);
+#pragma unroll 1
+            for (int m = 0; m < 2; ++m)
+                scores(m);
+#pragma unroll 1
             for (int j = 0; j < count; ++j) {
                 const bool more = j + 1 < count;
                 if (more)
                     advance();
-                output(0, j, begin);
-                if (more)
-                    scores(0);
-                output(1, j, begin);
-                if (more)
-                    scores(1);
+#pragma unroll 1
+                for (int m = 0; m < 2; ++m) {
+                    output(m, j, begin);
+                    if (more)
+                        scores(m);
+                }
                 begin = begin_next;
                 begin_next = last_of_seg;
             }
@@ -815,18 +811,14 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                     const int vst = c % kVs, vb = c % kVb;
                     wait(sh.v_full[vst], (c / kVs) & 1);
                     const uint8_t *src = mem + kVAt + vst * kTileBytes + t128 * kHd;
-                    uint4 raw[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        raw[k] = dead ? make_uint4(0, 0, 0, 0)
-                                      : *reinterpret_cast<const uint4 *>(src + ((k ^ (t128 & 7)) << 4));
-                    arrive(sh.v_free[vst]);
                     if (c >= kVb)
                         wait(sh.b_free[vb], (c / kVb - 1) & 1);
                     uint8_t *dst = mem + kBAt + vb * 2 * kTileBytes + (t128 >> 3) * 1024 + (t128 & 7) * 128;
-#pragma unroll
+#pragma unroll 1
                     for (int k = 0; k < 8; ++k) {
-                        const uint32_t in[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+                        const uint4 raw = dead ? make_uint4(0, 0, 0, 0)
+                                               : *reinterpret_cast<const uint4 *>(src + ((k ^ (t128 & 7)) << 4));
+                        const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
                         uint32_t o[8];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -846,6 +838,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                         *reinterpret_cast<uint4 *>(half + (((p0 + 1) ^ (t128 & 7)) << 4)) =
                             make_uint4(o[4], o[5], o[6], o[7]);
                     }
+                    arrive(sh.v_free[vst]);
                     tc::fence_smem_to_async();
                     arrive(sh.b_full[vb]);
                 }
