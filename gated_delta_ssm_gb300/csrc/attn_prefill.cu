@@ -19,9 +19,10 @@
 // equal contiguous shares, and q blocks that span shares are joined by a second
 // kernel, so causal and ragged blocks of any number fill the GPU.
 //
-// Roles of a CTA (512 threads): warp 0 copies pages, warp 1 issues products,
-// warps 2-3 clear the outputs of sequences without keys, warps 4-7 and 8-11 hold
-// a row each of tiles A and B, warps 12-15 split q and convert V.
+// Roles of a CTA (512 threads): warp 0 copies pages, warps 1 and 2 issue the
+// products of tiles A and B, warp 3 clears the outputs of sequences without
+// keys, warps 4-7 and 8-11 hold a row each of tiles A and B, warps 12-15 split q
+// and convert V.
 #include "attn_tc.cuh"
 #include "cluster.cuh"
 #include "gdn_device.cuh"
@@ -46,7 +47,7 @@ constexpr float kSlack = 8.0f;                // log2 of what a weight may excee
 
 struct Shared {
     uint64_t k_full[kKs], k_free[kKs], v_full[kVs], v_free[kVs], b_full[kVb], b_free[kVb];
-    uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_done[2], drain;
+    uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_done[2], drain[2];
     uint32_t tmem;
     volatile int abort;
     int64_t warp_sum[kThreads / 32];
@@ -125,6 +126,13 @@ __device__ __forceinline__ Walk walk_start(const AttnArgs &A, const Shared &sh, 
     w.q = seq_blocks(A, w.b);
     w.cut(A);
     return w;
+}
+
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // 32 columns of this thread's lane, without waiting; tmem_wait makes them usable.
@@ -216,25 +224,30 @@ __device__ __forceinline__ float row_max(uint32_t s_at, M mask_of, F factor, flo
 {
     float top = -INFINITY;
 #pragma unroll 1
-    for (int q4 = 0; q4 < 4; ++q4) {
-        uint32_t v[32];
-        tmem_get32(s_at + 32 * q4, v);
-        tmem_wait32(v);
-        const uint32_t mask = WHOLE ? 0xffffffffu : mask_of(q4);
+    for (int q2 = 0; q2 < 2; ++q2) {
+        uint32_t v[2][32];
+        tmem_get32(s_at + 64 * q2, v[0]);
+        tmem_get32(s_at + 64 * q2 + 32, v[1]);
+        tmem_wait32(v[0]);
+        tmem_wait32(v[1]);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            float mx[4];
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t mask = WHOLE ? 0xffffffffu : mask_of(2 * q2 + i);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                float s = __uint_as_float(v[16 * half + e]);
-                if (!WHOLE)
-                    s = (mask >> (16 * half + e)) & 1 ? s : -INFINITY;
-                mx[e & 3] = e < 4 ? s : fmaxf(mx[e & 3], s);
+            for (int half = 0; half < 2; ++half) {
+                float mx[2];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float s = __uint_as_float(v[i][16 * half + e]);
+                    if (!WHOLE)
+                        s = (mask >> (16 * half + e)) & 1 ? s : -INFINITY;
+                    mx[e & 1] = e < 2 ? s : fmaxf(mx[e & 1], s);
+                }
+                const float most = fmaxf(mx[0], mx[1]);
+                const float fk = factor(4 * q2 + 2 * i + half);
+                const float sc = score<CAP>(most, fk, cap2, inv_cap2);
+                top = fmaxf(top, WHOLE || most > -INFINITY ? sc : -INFINITY);
             }
-            const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            const float fk = factor(2 * q4 + half);
-            const float sc = score<CAP>(most, fk, cap2, inv_cap2);
-            top = fmaxf(top, WHOLE || most > -INFINITY ? sc : -INFINITY);
         }
     }
     return top;
@@ -300,19 +313,19 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
     if (tid == 0) {
         auto init = [&](uint64_t &bar, uint32_t n) { tc::mbar_init(tc::smem_addr(&bar), n); };
         for (int i = 0; i < kKs; ++i)
-            init(sh.k_full[i], 1), init(sh.k_free[i], 1);
+            init(sh.k_full[i], 1), init(sh.k_free[i], 2);
         for (int i = 0; i < kVs; ++i)
             init(sh.v_full[i], 1), init(sh.v_free[i], 128);
         for (int i = 0; i < kVb; ++i)
-            init(sh.b_full[i], 128), init(sh.b_free[i], 1);
+            init(sh.b_full[i], 128), init(sh.b_free[i], 2);
         for (int i = 0; i < 2; ++i) {
             init(sh.q_full[i], 128);
             init(sh.q_free[i], 129);
             init(sh.s_full[i], 1);
             init(sh.p_full[i], 128);
             init(sh.o_done[i], 1);
+            init(sh.drain[i], 1);
         }
-        init(sh.drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sh.abort = 0;
         sh.start_b = 0;
@@ -499,98 +512,92 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                     tc::mbar_wait_ns(tc::smem_addr(&sh.v_full[k % kVs]), (k / kVs) & 1, lim);
             }
         }
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ products. A thread's products run
-        // in the order of their issue, so S of the next tile may be issued behind the product that
-        // reads P from the same columns.
-        if (works && lane == 0) {
+    } else if (warp < 3) {
+        // ------------------------------------------------------------ products: warp 1 those of tile A, warp
+        // 2 those of B. A thread's products run in the order of their issue, so S of the next tile may be
+        // issued behind the product that reads P from the same columns.
+        if (works) {
+            const int m = warp - 1;
+            const bool leader = elect_one();
             constexpr uint32_t idesc_s = idesc_e4m3(128, 128);
             constexpr uint32_t idesc_o = tc::idesc_f16(128, 128) | 1u << 7 | 1u << 10 | tc::kIdescTransB;
+            const uint32_t s_at = tmem + m * 128, o_at = tmem + 256 + m * 128;
+            const uint64_t q = tc::sdesc_sw128(base + kQAt + 2 * m * kTileBytes);
             Walk w = walk_start(A, sh, count);
-            int seg_a = 0, seg_b = 0;   // segment of the next scores of A, B
-            int c = 0;                  // the tile of scores: same for A and B
-            int t = w.t;
-            bool last_of_seg = t + 1 == w.end;
-            auto scores = [&](int m) {  // S of tile c
+            int seg = 0, t = w.t, c = 0;      // the next tile of scores
+            bool fresh = true, begin = true;  // that tile, and the one of the next output, begins its segment
+            auto scores = [&] {
                 const int ks = c % kKs;
-                wait1(sh.q_full[m], (m ? seg_b : seg_a) & 1);
-                wait1(sh.k_full[ks], (c / kKs) & 1);
+                if (fresh)
+                    wait(sh.q_full[m], seg & 1);
+                wait(sh.k_full[ks], (c / kKs) & 1);
                 tc::fence_after_sync();
-                if (!sh.abort) {
-                    const uint64_t k = tc::sdesc_sw128(base + kKAt + ks * kTileBytes);
-#pragma unroll 1
-                    for (int part = 0; part < 2; ++part) {
-                        const uint64_t q = tc::sdesc_sw128(base + kQAt + (2 * m + part) * kTileBytes);
+                const bool last = t + 1 == w.end;
+                if (leader) {
+                    if (!sh.abort) {
+                        const uint64_t k = tc::sdesc_sw128(base + kKAt + ks * kTileBytes);
 #pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            mma_e4m3(tmem + m * 128, q + 2 * s, k + 2 * s, idesc_s, part + s > 0);
+                        for (int part = 0; part < 2; ++part)
+#pragma unroll
+                            for (int s = 0; s < 4; ++s)   // 32 bytes of the rows at a time
+                                mma_e4m3(s_at, q + part * (kTileBytes >> 4) + 2 * s, k + 2 * s, idesc_s,
+                                         part + s > 0);
                     }
-                }
-                tc::mma_commit(tc::smem_addr(&sh.s_full[m]));
-                if (last_of_seg) {
-                    tc::mma_commit(tc::smem_addr(&sh.q_free[m]));
-                    m ? ++seg_b : ++seg_a;
-                }
-                if (m == 1)
+                    tc::mma_commit(tc::smem_addr(&sh.s_full[m]));
                     tc::mma_commit(tc::smem_addr(&sh.k_free[ks]));
-            };
-            auto advance = [&] {        // to the next tile of scores
-                ++c;
-                if (++t == w.end && w.next(A))
-                    t = w.t;
-                last_of_seg = t + 1 == w.end;
-            };
-            auto output = [&](int m, int j, bool begin) {   // O += P V of tile j
-                wait1(sh.b_full[j % kVb], (j / kVb) & 1);
-                wait1(sh.p_full[m], j & 1);
-                tc::fence_after_sync();
-                if (!sh.abort) {
-                    const uint64_t v =
-                        tc::sdesc_sw128_mn(base + kBAt + (j % kVb) * 2 * kTileBytes, kTileBytes, 1024);
-#pragma unroll 2
-                    for (int s = 0; s < 8; ++s)   // 16 keys: 8 columns of P, 2 KB of V
-                        tc::mma_f16_ta(tmem + 256 + m * 128, tmem + m * 128 + 8 * s, v + 128 * s, idesc_o,
-                                       !begin || s > 0);
+                    if (last)
+                        tc::mma_commit(tc::smem_addr(&sh.q_free[m]));
                 }
-                tc::mma_commit(tc::smem_addr(&sh.o_done[m]));
-                if (m == 1)
-                    tc::mma_commit(tc::smem_addr(&sh.b_free[j % kVb]));
+                __syncwarp();
+                ++c;
+                fresh = last;
+                if (last) {
+                    ++seg;
+                    t = w.next(A) ? w.t : 0;
+                } else {
+                    ++t;
+                }
             };
-            bool begin = true, begin_next = last_of_seg;
-#pragma unroll 1
-            for (int m = 0; m < 2; ++m)
-                scores(m);
+            scores();
 #pragma unroll 1
             for (int j = 0; j < count; ++j) {
-                const bool more = j + 1 < count;
-                if (more)
-                    advance();
-#pragma unroll 1
-                for (int m = 0; m < 2; ++m) {
-                    output(m, j, begin);
-                    if (more)
-                        scores(m);
+                const bool next_begin = fresh;
+                wait(sh.b_full[j % kVb], (j / kVb) & 1);
+                wait(sh.p_full[m], j & 1);
+                tc::fence_after_sync();
+                if (leader) {
+                    if (!sh.abort) {
+                        const uint64_t v =
+                            tc::sdesc_sw128_mn(base + kBAt + (j % kVb) * 2 * kTileBytes, kTileBytes, 1024);
+#pragma unroll
+                        for (int s = 0; s < 8; ++s)   // 16 keys: 8 columns of P, 2 KB of V
+                            tc::mma_f16_ta(o_at, s_at + 8 * s, v + 128 * s, idesc_o, s > 0 || !begin);
+                    }
+                    tc::mma_commit(tc::smem_addr(&sh.o_done[m]));
+                    tc::mma_commit(tc::smem_addr(&sh.b_free[j % kVb]));
                 }
-                begin = begin_next;
-                begin_next = last_of_seg;
+                __syncwarp();
+                begin = next_begin;
+                if (c < count)
+                    scores();
             }
-            if (sh.abort) {   // products in flight end before the tensor memory is freed
-                tc::mma_commit(tc::smem_addr(&sh.drain));
-                tc::mbar_wait_ns(tc::smem_addr(&sh.drain), 0, lim);
+            if (sh.abort && leader) {   // products in flight end before the tensor memory is freed
+                tc::mma_commit(tc::smem_addr(&sh.drain[m]));
+                tc::mbar_wait_ns(tc::smem_addr(&sh.drain[m]), 0, lim);
             }
+            __syncwarp();
         }
-        __syncwarp();
-    } else if (warp < 4) {
+    } else if (warp == 3) {
         // ------------------------------------------------------------ sequences without keys
-        const int t64 = tid - 64;
+        const int t32 = lane;
         for (int b = blockIdx.x; b < B.n_seq; b += gridDim.x) {
             const Blocks q = seq_blocks(A, b);
-            if (!q.s.ok && t64 == 0)
+            if (!q.s.ok && t32 == 0)
                 atomicOr(&g_attn_prefill_error, kErrMeta);
             if (q.s.ok && q.n == 0) {
                 uint4 *o = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(A.out) +
                                                      (int64_t)q.s.row0 * B.Hq * kHd);
-                for (int64_t e = t64; e < (int64_t)q.s.n * B.Hq * (kHd / 8); e += 64)
+                for (int64_t e = t32; e < (int64_t)q.s.n * B.Hq * (kHd / 8); e += 32)
                     o[e] = make_uint4(0, 0, 0, 0);
             }
         }
