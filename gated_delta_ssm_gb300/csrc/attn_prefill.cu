@@ -21,8 +21,8 @@
 //
 // Roles of a CTA (512 threads): warp 0 copies pages, warps 1 and 2 issue the
 // products of tiles A and B, warp 3 clears the outputs of sequences without
-// keys, warps 4-7 and 8-11 hold a row each of tiles A and B, warps 12-15 split q
-// and convert V.
+// keys, warps 4-7 and 8-11 split q and hold a row each of tiles A and B, warps
+// 12-15 convert V.
 #include "attn_tc.cuh"
 #include "cluster.cuh"
 #include "gdn_device.cuh"
@@ -43,11 +43,13 @@ constexpr uint32_t kVAt = kKAt + kKs * kTileBytes;
 constexpr uint32_t kBAt = kVAt + kVs * kTileBytes;
 constexpr uint32_t kEnd = kBAt + kVb * 2 * kTileBytes;
 constexpr uint32_t kTmemCols = 512;           // S of A, S of B, O of A, O of B: 128 each
-constexpr float kSlack = 8.0f;                // log2 of what a weight may exceed 1 by
+// The reference moves when a row's weights of one tile sum to more than this: weights and sums are floating
+// numbers of 8 exponent bits, so a reference that lags behind costs no precision, only range.
+constexpr float kSlack = 8.0f, kSlackSum = 65536.0f;   // 128 weights of at most 2^8 sum to 2^15
 
 struct Shared {
     uint64_t k_full[kKs], k_free[kKs], v_full[kVs], v_free[kVs], b_full[kVb], b_free[kVb];
-    uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_done[2], drain[2];
+    uint64_t q_full[2], s_full[2], p_full[2], o_done[2], drain[2];
     uint32_t tmem;
     volatile int abort;
     int64_t warp_sum[kThreads / 32];
@@ -217,6 +219,78 @@ __device__ __forceinline__ float2 unpack2(uint64_t a)
     return d;
 }
 
+// 16 columns of this thread's lane, without waiting, and the wait for them.
+__device__ __forceinline__ void tmem_get16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+                   "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :: "memory");
+}
+
+// Weights of a row that sees the whole tile, against the reference as it is: one pass, no maximum. They are
+// stored if every row of the warp stayed within 2^kSlack summed; otherwise the scores are left as they were
+// and the caller takes the form that moves the reference.
+template <bool CAP, typename F>
+__device__ __forceinline__ bool row_weights_once(uint32_t s_at, F factor, float ref, float &l, float cap2,
+                                                 float inv_cap2)
+{
+    uint32_t x[2][16], y[64];
+    uint64_t sum[2] = {0, 0};
+    const uint64_t sub2 = pack2(-ref, -ref);
+    tmem_get16(s_at, x[0]);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        uint32_t(&v)[16] = x[c & 1];
+        tmem_wait16(v);
+        if (c < 7)
+            tmem_get16(s_at + 16 * (c + 1), x[(c + 1) & 1]);
+        const float fk = factor(c);
+        const uint64_t fk2 = pack2(fk, fk);
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+            const float s0 = __uint_as_float(v[e]), s1 = __uint_as_float(v[e + 1]);
+            float2 z;
+            if constexpr (CAP) {
+                z.x = score<CAP>(s0, fk, cap2, inv_cap2) - ref;
+                z.y = score<CAP>(s1, fk, cap2, inv_cap2) - ref;
+            } else {
+                z = unpack2(fma2(pack2(s0, s1), fk2, sub2));
+            }
+            z.x = ex2(z.x);
+            z.y = ex2(z.y);
+            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pack2(z.x, z.y));
+            y[8 * c + e / 2] = pack_bf16x2(z.x, z.y);
+        }
+    }
+    const float2 t = unpack2(add2(sum[0], sum[1]));
+    const float add = t.x + t.y;
+    if (!__all_sync(0xffffffffu, add <= kSlackSum))
+        return false;
+    l += add;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        tc::tmem_st16u(s_at + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(y + 16 * c));
+    return true;
+}
+
+// 16 bytes to shared memory without passing through registers; zeros where `have` is false.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool have)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(have ? 16 : 0)
+                 : "memory");
+}
+
 // The largest visible score of this thread's row of the tile (128 columns at s_at), -inf for none. The cap
 // is monotonic and factors are not negative, so each 16 columns' raw maximum stands for them.
 template <bool CAP, bool WHOLE, typename M, typename F>
@@ -320,7 +394,6 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
             init(sh.b_full[i], 128), init(sh.b_free[i], 2);
         for (int i = 0; i < 2; ++i) {
             init(sh.q_full[i], 128);
-            init(sh.q_free[i], 129);
             init(sh.s_full[i], 1);
             init(sh.p_full[i], 128);
             init(sh.o_done[i], 1);
@@ -525,61 +598,65 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
             const uint64_t q = tc::sdesc_sw128(base + kQAt + 2 * m * kTileBytes);
             Walk w = walk_start(A, sh, count);
             int seg = 0, t = w.t, c = 0;      // the next tile of scores
-            bool fresh = true, begin = true;  // that tile, and the one of the next output, begins its segment
-            auto scores = [&] {
+            bool fresh = true, begin = true;  // whether it, and the tile of the next output, begins its segment
+            auto issue_scores = [&] {         // by one thread
                 const int ks = c % kKs;
-                if (fresh)
-                    wait(sh.q_full[m], seg & 1);
-                wait(sh.k_full[ks], (c / kKs) & 1);
-                tc::fence_after_sync();
-                const bool last = t + 1 == w.end;
-                if (leader) {
-                    if (!sh.abort) {
-                        const uint64_t k = tc::sdesc_sw128(base + kKAt + ks * kTileBytes);
+                if (!sh.abort) {
+                    const uint64_t k = tc::sdesc_sw128(base + kKAt + ks * kTileBytes);
 #pragma unroll
-                        for (int part = 0; part < 2; ++part)
+                    for (int part = 0; part < 2; ++part)
 #pragma unroll
-                            for (int s = 0; s < 4; ++s)   // 32 bytes of the rows at a time
-                                mma_e4m3(s_at, q + part * (kTileBytes >> 4) + 2 * s, k + 2 * s, idesc_s,
-                                         part + s > 0);
-                    }
-                    tc::mma_commit(tc::smem_addr(&sh.s_full[m]));
-                    tc::mma_commit(tc::smem_addr(&sh.k_free[ks]));
-                    if (last)
-                        tc::mma_commit(tc::smem_addr(&sh.q_free[m]));
+                        for (int s = 0; s < 4; ++s)   // 32 bytes of the rows at a time
+                            mma_e4m3(s_at, q + part * (kTileBytes >> 4) + 2 * s, k + 2 * s, idesc_s,
+                                     part + s > 0);
                 }
-                __syncwarp();
+                tc::mma_commit(tc::smem_addr(&sh.s_full[m]));
+                tc::mma_commit(tc::smem_addr(&sh.k_free[ks]));
+            };
+            auto advance = [&] {
                 ++c;
-                fresh = last;
-                if (last) {
+                fresh = ++t == w.end;
+                if (fresh) {
                     ++seg;
-                    t = w.next(A) ? w.t : 0;
-                } else {
-                    ++t;
+                    if (w.next(A))
+                        t = w.t;
                 }
             };
-            scores();
 #pragma unroll 1
-            for (int j = 0; j < count; ++j) {
-                const bool next_begin = fresh;
-                wait(sh.b_full[j % kVb], (j / kVb) & 1);
-                wait(sh.p_full[m], j & 1);
-                tc::fence_after_sync();
-                if (leader) {
-                    if (!sh.abort) {
-                        const uint64_t v =
-                            tc::sdesc_sw128_mn(base + kBAt + (j % kVb) * 2 * kTileBytes, kTileBytes, 1024);
+            for (int j = -1; j < count; ++j) {   // output of tile j, scores of tile j + 1
+                const bool more = c < count;
+                if (more)
+                    wait(sh.k_full[c % kKs], (c / kKs) & 1);
+                if (j >= 0) {
+                    const int vb = j % kVb;
+                    wait(sh.b_full[vb], (j / kVb) & 1);
+                    wait(sh.p_full[m], j & 1);
+                    tc::fence_after_sync();
+                    if (leader) {
+                        if (!sh.abort) {
+                            const uint64_t v = tc::sdesc_sw128_mn(base + kBAt + vb * 2 * kTileBytes, kTileBytes, 1024);
 #pragma unroll
-                        for (int s = 0; s < 8; ++s)   // 16 keys: 8 columns of P, 2 KB of V
-                            tc::mma_f16_ta(o_at, s_at + 8 * s, v + 128 * s, idesc_o, s > 0 || !begin);
+                            for (int s = 0; s < 8; ++s)   // 16 keys: 8 columns of P, 2 KB of V
+                                tc::mma_f16_ta(o_at, s_at + 8 * s, v + 128 * s, idesc_o, s > 0 || !begin);
+                        }
+                        if (more && !fresh)
+                            issue_scores();
+                        tc::mma_commit(tc::smem_addr(&sh.o_done[m]));
+                        tc::mma_commit(tc::smem_addr(&sh.b_free[vb]));
                     }
-                    tc::mma_commit(tc::smem_addr(&sh.o_done[m]));
-                    tc::mma_commit(tc::smem_addr(&sh.b_free[j % kVb]));
+                    __syncwarp();
+                    begin = fresh;
                 }
-                __syncwarp();
-                begin = next_begin;
-                if (c < count)
-                    scores();
+                if (more) {
+                    if (fresh) {
+                        wait(sh.q_full[m], seg & 1);
+                        tc::fence_after_sync();
+                        if (leader)
+                            issue_scores();
+                        __syncwarp();
+                    }
+                    advance();
+                }
             }
             if (sh.abort && leader) {   // products in flight end before the tensor memory is freed
                 tc::mma_commit(tc::smem_addr(&sh.drain[m]));
@@ -611,7 +688,53 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
             const int per_tile = kTile / B.P;
             const float cap2 = A.softcap * kLog2e, inv_cap2 = CAP ? 1.0f / cap2 : 0.0f;
             Walk w = walk_start(A, sh, count);
-            int c = 0, seg = 0;
+            int c = 0;
+            const float sign = A.scale < 0.0f ? -1.0f : 1.0f;
+            // The q rows of the segment that w is at, 32 by each warp. A row's bf16 pieces land where its own
+            // two e4m3 rows will lie, dimensions 0-63 in hi's place and 64-127 in lo's.
+            auto load_q = [&] {
+                const uint32_t at = kQAt + 2 * m * kTileBytes;
+                const int row_w = (warp & 3) * 32;
+#pragma unroll 4
+                for (int e = lane; e < 32 * 16; e += 32) {
+                    const int rr = row_w + (e >> 4), piece = e & 15;
+                    const int r = w.i * kRows + m * 128 + rr, tok = r / B.G, gh = r - tok * B.G;
+                    const bool have = tok < w.q.s.n;
+                    const __nv_bfloat16 *src =
+                        static_cast<const __nv_bfloat16 *>(A.q) +
+                        (have ? (int64_t)(w.q.s.row0 + tok) * A.q_stride + (w.h * B.G + gh) * kHd + piece * 8 : 0);
+                    copy16(base + at + (piece >> 3) * kTileBytes + (rr >> 3) * 1024 + (rr & 7) * 128 +
+                               (((piece & 7) ^ (rr & 7)) << 4),
+                           src, have);
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                __syncwarp();
+                const int u = lane & 7;
+#pragma unroll 1
+                for (int rr = row_w + (lane >> 3); rr < row_w + 32; rr += 4) {
+                    uint8_t *at_row = mem + at + (rr >> 3) * 1024 + (rr & 7) * 128;
+                    const uint8_t *raw = at_row + (u >> 2) * kTileBytes;   // elements 16 u ..: pieces 2 u, 2 u + 1
+                    float v[16];
+                    unpack_q16(*reinterpret_cast<const uint4 *>(raw + ((((2 * u) & 7) ^ (rr & 7)) << 4)),
+                               *reinterpret_cast<const uint4 *>(raw + ((((2 * u + 1) & 7) ^ (rr & 7)) << 4)), v);
+                    float top = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        top = fmaxf(top, fabsf(v[e]));
+#pragma unroll
+                    for (int k = 1; k < 8; k <<= 1)
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+                    __syncwarp();   // the row is read before it is overwritten
+                    store_q16(at_row + ((u ^ (rr & 7)) << 4), kTileBytes, v, sign * q_factor(top));
+                    if (u == 0)
+                        sh.f[m][rr] = fabsf(A.scale) * kLog2e * pow2i(-q_exponent(top));
+                }
+                tc::fence_smem_to_async();
+                __syncwarp();
+                arrive(sh.q_full[m]);
+            };
+            load_q();
+            bool more = true;
             do {
                 const int r = w.i * kRows + m * 128 + row;       // row of the sequence and head
                 const int tok = r / B.G;
@@ -636,7 +759,6 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                 };
                 int p_far = page_at(w.t + 1);
                 float ks_next = scale_at(page_at(w.t));
-                wait(sh.q_full[m], seg & 1);
                 const float f = sh.f[m][row];
                 float ref = -INFINITY, l = 0.0f;
                 for (int t = w.t; t < w.end; ++t, ++c) {
@@ -663,54 +785,64 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                     };
                     wait(sh.s_full[m], c & 1);
                     tc::fence_after_sync();
-                    float top = -INFINITY;
-                    if (whole)
-                        top = row_max<CAP, true>(s_at, mask_of, factor, cap2, inv_cap2);
-                    else
-                        top = row_max<CAP, false>(s_at, mask_of, factor, cap2, inv_cap2);
-                    // the reference moves when a weight would pass 2^kSlack, or is the row's first
-                    const bool move = top > ref + kSlack || (ref == -INFINITY && top > ref);
-                    if (__any_sync(0xffffffffu, move)) {
-                        const float to = move ? top : ref;
-                        const float a = move ? ex2(ref - to) : 1.0f;
-                        ref = to;
-                        l *= a;
-                        if (t > w.t) {
-                            wait(sh.o_done[m], (c - 1) & 1);
-                            tc::fence_after_sync();
-#pragma unroll 1
-                            for (int q4 = 0; q4 < 4; ++q4) {
-                                uint32_t x[32];
-                                tmem_get32(o_at + 32 * q4, x);
-                                tmem_wait32(x);
-#pragma unroll
-                                for (int half = 0; half < 2; ++half) {
-                                    uint32_t y[16];
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e)
-                                        y[e] = __float_as_uint(__uint_as_float(x[16 * half + e]) * a);
-                                    tc::tmem_st16u(o_at + 32 * q4 + 16 * half, y);
+                    if (!whole || !__all_sync(0xffffffffu, ref > -INFINITY) ||
+                        !row_weights_once<CAP>(s_at, factor, ref, l, cap2, inv_cap2)) {
+                        float top = -INFINITY;
+                        if (whole)
+                            top = row_max<CAP, true>(s_at, mask_of, factor, cap2, inv_cap2);
+                        else
+                            top = row_max<CAP, false>(s_at, mask_of, factor, cap2, inv_cap2);
+                        // the reference moves when a weight would pass 2^kSlack, or is the row's first
+                        const bool move = top > ref + kSlack || (ref == -INFINITY && top > ref);
+                        if (__any_sync(0xffffffffu, move)) {
+                            const float to = move ? top : ref;
+                            const float a = move ? ex2(ref - to) : 1.0f;
+                            ref = to;
+                            l *= a;
+                            if (t > w.t) {
+                                wait(sh.o_done[m], (c - 1) & 1);
+                                tc::fence_after_sync();
+    #pragma unroll 1
+                                for (int q4 = 0; q4 < 4; ++q4) {
+                                    uint32_t x[32];
+                                    tmem_get32(o_at + 32 * q4, x);
+                                    tmem_wait32(x);
+    #pragma unroll
+                                    for (int half = 0; half < 2; ++half) {
+                                        uint32_t y[16];
+    #pragma unroll
+                                        for (int e = 0; e < 16; ++e)
+                                            y[e] = __float_as_uint(__uint_as_float(x[16 * half + e]) * a);
+                                        tc::tmem_st16u(o_at + 32 * q4 + 16 * half, y);
+                                    }
                                 }
                             }
                         }
+                        const float sub = ref == -INFINITY ? 0.0f : ref;
+                        if (whole)
+                            l += row_weights<CAP, true>(s_at, mask_of, factor, sub, cap2, inv_cap2);
+                        else
+                            l += row_weights<CAP, false>(s_at, mask_of, factor, sub, cap2, inv_cap2);
                     }
-                    const float sub = ref == -INFINITY ? 0.0f : ref;
-                    if (whole)
-                        l += row_weights<CAP, true>(s_at, mask_of, factor, sub, cap2, inv_cap2);
-                    else
-                        l += row_weights<CAP, false>(s_at, mask_of, factor, sub, cap2, inv_cap2);
                     tc::tmem_wait_st();
                     tc::fence_before_sync();
                     arrive(sh.p_full[m]);
                 }
-                arrive(sh.q_free[m]);
+                // The products that read the segment's q are done (its last scores are here): the next
+                // segment's q goes in, and its first scores are formed while this one's rows are written.
+                const bool whole_block = w.begins() && w.ends(), begins = w.begins();
+                const int seg_b = w.b, seg_h = w.h, seg_row = w.i * kRows, seg_row0 = w.q.s.row0;
+                const int64_t end_unit = first + count - w.left + (w.n - w.t);   // past the block's last tile
+                more = w.next(A);
+                if (more)
+                    load_q();
                 wait(sh.o_done[m], (c - 1) & 1);
                 tc::fence_after_sync();
-                if (w.begins() && w.ends()) {
+                if (whole_block) {
                     const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
                     const int gh = r - tok * B.G;
-                    uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(A.out) +
-                                                           ((int64_t)(w.q.s.row0 + tok) * B.Hq + w.h * B.G + gh) * kHd);
+                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(A.out) +
+                                         ((int64_t)(seg_row0 + tok) * B.Hq + seg_h * B.G + gh) * kHd;
 #pragma unroll 1
                     for (int q4 = 0; q4 < 4; ++q4) {
                         uint32_t x[32];
@@ -718,18 +850,20 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                         tmem_wait32(x);
                         if (live) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                uint32_t y[4];
+                            for (int e = 0; e < 2; ++e) {
+                                uint32_t y[8];
 #pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    y[i] = pack_bf16x2(__uint_as_float(x[8 * e + 2 * i]) * inv,
-                                                       __uint_as_float(x[8 * e + 2 * i + 1]) * inv);
-                                out[4 * q4 + e] = make_uint4(y[0], y[1], y[2], y[3]);
+                                for (int i = 0; i < 8; ++i)
+                                    y[i] = pack_bf16x2(__uint_as_float(x[16 * e + 2 * i]) * inv,
+                                                       __uint_as_float(x[16 * e + 2 * i + 1]) * inv);
+                                uint4 *at = reinterpret_cast<uint4 *>(out + 32 * q4 + 16 * e);
+                                at[0] = make_uint4(y[0], y[1], y[2], y[3]);
+                                at[1] = make_uint4(y[4], y[5], y[6], y[7]);
                             }
                         }
                     }
                 } else {
-                    const int slot = 2 * blockIdx.x + (w.begins() ? 1 : 0);
+                    const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
                     float *dst = parts + ((size_t)slot * kRows + m * 128 + row) * kPartRow;
 #pragma unroll 1
                     for (int q4 = 0; q4 < 4; ++q4) {
@@ -742,52 +876,19 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                                 make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
                     }
                     *reinterpret_cast<float2 *>(dst + kHd) = make_float2(l, ref);
-                    if (w.begins() && m == 0 && row == 0) {
-                        const int64_t end_unit = first + count - w.left + (w.n - w.t);   // past its last tile
-                        meta[blockIdx.x] = {w.b, w.h, w.i * kRows, share_of(total, n_cta, end_unit - 1), 1, {}};
-                    }
+                    if (begins && m == 0 && row == 0)
+                        meta[blockIdx.x] = {seg_b, seg_h, seg_row, share_of(total, n_cta, end_unit - 1), 1, {}};
                 }
                 tc::fence_before_sync();
-                ++seg;
-            } while (w.next(A));
+            } while (more);
         }
     } else {
-        // ------------------------------------------------------------ q rows and V
+        // ------------------------------------------------------------ V to bf16: a key per thread
         if (works) {
-            const int t128 = tid - 384, u = t128 & 7, r16 = t128 >> 3;
+            const int t128 = tid - 384;
             Walk w = walk_start(A, sh, count);
-            int c = 0, seg = 0;
-            const float sign = A.scale < 0.0f ? -1.0f : 1.0f;
+            int c = 0;
             do {
-#pragma unroll 1
-                for (int m = 0; m < 2; ++m) {
-                    if (seg >= 1)
-                        wait(sh.q_free[m], (seg - 1) & 1);
-#pragma unroll 2
-                    for (int rr = r16; rr < 128; rr += 16) {
-                        const int r = w.i * kRows + m * 128 + rr, tok = r / B.G, gh = r - tok * B.G;
-                        float v[16] = {};
-                        if (tok < w.q.s.n)
-                            load_q16(static_cast<const __nv_bfloat16 *>(A.q) +
-                                         (int64_t)(w.q.s.row0 + tok) * A.q_stride + (w.h * B.G + gh) * kHd + u * 16,
-                                     v);
-                        float top = 0.0f;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            top = fmaxf(top, fabsf(v[e]));
-#pragma unroll
-                        for (int k = 1; k < 8; k <<= 1)
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-                        store_q16(mem + kQAt + 2 * m * kTileBytes + (rr >> 3) * 1024 + (rr & 7) * 128 +
-                                      ((u ^ (rr & 7)) << 4),
-                                  kTileBytes, v, sign * q_factor(top));
-                        if (u == 0)
-                            sh.f[m][rr] = fabsf(A.scale) * kLog2e * pow2i(-q_exponent(top));
-                    }
-                    tc::fence_smem_to_async();
-                    arrive(sh.q_full[m]);
-                }
-                // V: a key per thread
                 const int32_t *table = B.page_table + (int64_t)w.b * B.max_pages;
                 const int tok1 = min((w.i * kRows + kRows - 1) / B.G, w.q.s.n - 1);
                 const int j_lo = max(0, w.q.first + w.i * kRows / B.G - A.window + 1);
@@ -849,7 +950,6 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                     tc::fence_smem_to_async();
                     arrive(sh.b_full[vb]);
                 }
-                ++seg;
             } while (w.next(A));
         }
     }

@@ -68,19 +68,22 @@ __device__ __forceinline__ void split_e4m3(float x, float y, uint32_t &hi, uint3
     lo = __nv_cvt_float2_to_fp8x2(make_float2(x - back.x, y - back.y), __NV_SATFINITE, __NV_E4M3);
 }
 
-// 16 elements of a q row (16 bytes aligned), bf16 to float.
+// 16 bf16 elements as floats.
+__device__ __forceinline__ void unpack_q16(uint4 a, uint4 b, float (&v)[16])
+{
+    const uint32_t y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        v[2 * e] = __uint_as_float(y[e] << 16);
+        v[2 * e + 1] = __uint_as_float(y[e] & 0xffff0000u);
+    }
+}
+
+// 16 elements of a q row (16-byte aligned).
 __device__ __forceinline__ void load_q16(const __nv_bfloat16 *p, float (&v)[16])
 {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p) + c);
-        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[8 * c + 2 * e] = __uint_as_float(y[e] << 16);
-            v[8 * c + 2 * e + 1] = __uint_as_float(y[e] & 0xffff0000u);
-        }
-    }
+    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p)), b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+    unpack_q16(a, b, v);
 }
 
 // x with 2^x top in [128, 256) (0 for top = 0); at most 126, so that 2^x stays finite.
