@@ -1,0 +1,280 @@
+// attn_share.cuh -- how the attention kernels share out a ragged batch.
+//
+// Work is counted in units of (block of q rows, tile of 128 keys): a sequence's rows, one per (token, head of
+// the group) of a KV head, are cut into blocks, and a block meets the key tiles that its rows can see. A block
+// counts OVER units on top, ahead of its tiles, for what it costs besides them (its q rows, its output). The
+// units of the batch, in the order (sequence, KV head, block, tile), are cut into equal contiguous shares, one
+// per CTA, whatever the lengths are; the lengths live on the device, so every CTA counts them itself. One warp
+// of a CTA then walks the share and hands the other warps its segments (a block and a run of its tiles) through
+// a ring in shared memory; that keeps the walk's code, sequence loads and divisions out of their loops.
+#pragma once
+
+#include "attn_device.cuh"
+#include "tc_ptx.cuh"
+
+namespace gdn {
+namespace attn {
+
+constexpr int kTile = 128;            // keys per tile
+constexpr int kNoWindow = 1 << 30;    // positions are below this
+constexpr int kRing = 4;
+
+// A run of key tiles of one block of q rows.
+struct Seg {
+    int nt, kt;               // tiles (0: the share is done), the first one's index
+    int b, h;
+    int row0, n, first;       // the sequence's token rows, tokens in the call, position of its first row
+    int lo, hi;               // key positions that any row of the block sees
+    int blk, tok0, rem0;      // the block's first row (token * G + head of the group), its token and head
+    int begins, whole;        // whether the run holds the block's first tile; all of its tiles
+    int last_cta;             // the CTA whose share holds the block's last tile
+    int pad;
+};
+static_assert(sizeof(Seg) == 64, "copied as four 16-byte pieces");
+
+struct Ring {
+    Seg seg[kRing];
+    uint64_t full[kRing], free[kRing];
+};
+
+template <int THREADS>
+struct ShareShared {
+    int64_t warp_sum[THREADS / 32];
+    int64_t start_off, head_units;    // the share's first unit within its sequence; units of one KV head there
+    int start_b;
+};
+
+struct Share {
+    int64_t total, first;             // units of the batch; the share's first
+    int n_cta, count;                 // CTAs with a share; units of this one's
+};
+
+__device__ __forceinline__ int64_t share_begin(int64_t total, int n, int c) { return total * c / n; }
+__device__ __forceinline__ int share_of(int64_t total, int n, int64_t unit)
+{
+    return (int)(((unit + 1) * n - 1) / total);
+}
+
+// Blocks of a sequence; none where there are no keys.
+template <int ROWS>
+__device__ __forceinline__ int blocks_of(const Batch &B, const Seq &s)
+{
+    return s.L > 0 ? (int)(((int64_t)s.n * B.G + ROWS - 1) / ROWS) : 0;
+}
+
+// Key positions [lo, hi] that block i of a sequence sees, at least [0, 0].
+template <int ROWS>
+__device__ __forceinline__ void block_keys(const AttnArgs &A, const Seq &s, int i, int &lo, int &hi)
+{
+    const int G = A.b.G, first = s.L - s.n;
+    lo = max(0, first + i * ROWS / G - A.window + 1);
+    hi = max(0, first + min((i * ROWS + ROWS - 1) / G, s.n - 1));
+}
+
+template <int ROWS, int OVER>
+__device__ __forceinline__ int block_units(const AttnArgs &A, const Seq &s, int i)
+{
+    int lo, hi;
+    block_keys<ROWS>(A, s, i, lo, hi);
+    return hi / kTile - lo / kTile + 1 + OVER;
+}
+
+// Units of one KV head of a sequence: blocks from, from + step, ..
+template <int ROWS, int OVER>
+__device__ __forceinline__ int64_t head_units(const AttnArgs &A, int b, int from, int step)
+{
+    const Seq s = load_seq(A.b, b);
+    const int n = blocks_of<ROWS>(A.b, s);
+    int64_t u = 0;
+#pragma unroll 1
+    for (int i = from; i < n; i += step)
+        u += block_units<ROWS, OVER>(A, s, i);
+    return u;
+}
+
+// Count the batch and find where this CTA's share begins. Every thread of the CTA calls it.
+template <int THREADS, int ROWS, int OVER>
+__device__ __forceinline__ Share find_share(const AttnArgs &A, ShareShared<THREADS> &sh)
+{
+    const Batch &B = A.b;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // a group of g neighbouring lanes counts one sequence, or a thread several where there are many
+    int g = 1;
+    while (g < 32 && (int64_t)B.n_seq * g * 2 <= THREADS)
+        g *= 2;
+    const int per = g > 1 ? 1 : (B.n_seq + THREADS - 1) / THREADS;
+    const int first_b = (tid / g) * per, sub = tid % g;
+    int64_t mine = 0;
+#pragma unroll 1
+    for (int i = 0; i < per && first_b + i < B.n_seq; ++i)
+        mine += head_units<ROWS, OVER>(A, first_b + i, sub, g);
+    for (int m = 1; m < g; m <<= 1)
+        mine += __shfl_xor_sync(0xffffffffu, mine, m);
+    const int64_t one_head = mine;
+    mine = sub == 0 ? mine * B.Hkv : 0;
+    int64_t incl = mine;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, incl, m);
+        if (lane >= m)
+            incl += up;
+    }
+    if (lane == 31)
+        sh.warp_sum[warp] = incl;
+    __syncthreads();
+    Share r;
+    r.total = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+        incl += i < warp ? sh.warp_sum[i] : 0;
+        r.total += sh.warp_sum[i];
+    }
+    r.n_cta = (int)min((int64_t)gridDim.x, r.total);
+    const bool works = (int)blockIdx.x < r.n_cta;
+    r.first = works ? share_begin(r.total, r.n_cta, blockIdx.x) : 0;
+    r.count = works ? (int)(share_begin(r.total, r.n_cta, blockIdx.x + 1) - r.first) : 0;
+    if (works && r.first < incl && r.first >= incl - mine) {   // among this thread's sequences
+        int64_t at = incl - mine;
+#pragma unroll 1
+        for (int i = 0; i < per && first_b + i < B.n_seq; ++i) {
+            const int64_t u = g > 1 ? one_head : head_units<ROWS, OVER>(A, first_b + i, 0, 1);
+            if (r.first < at + u * B.Hkv) {
+                sh.start_b = first_b + i;
+                sh.start_off = r.first - at;
+                sh.head_units = u;
+                break;
+            }
+            at += u * B.Hkv;
+        }
+    }
+    __syncthreads();
+    return r;
+}
+
+// One warp walks the share and fills the ring; `wait` is the kernel's bounded wait.
+template <int THREADS, int ROWS, int OVER, typename W>
+__device__ __forceinline__ void walk_share(const AttnArgs &A, const ShareShared<THREADS> &sh, const Share &r,
+                                           Ring &ring, W wait)
+{
+    const Batch &B = A.b;
+    const int lane = threadIdx.x & 31;
+    int b = 0, h = 0, i = 0, t = 0, n = 0;
+    Seq s = {};
+    if (r.count > 0) {   // the block and tile of the first unit: each lane looks through a part of the blocks
+        b = sh.start_b;
+        s = load_seq(B, b);
+        n = blocks_of<ROWS>(B, s);
+        h = (int)(sh.start_off / sh.head_units);
+        const int64_t off = sh.start_off - h * sh.head_units;
+        const int each = (n + 31) / 32, i0 = min(n, lane * each), i1 = min(n, i0 + each);
+        int64_t u = 0;
+#pragma unroll 1
+        for (int k = i0; k < i1; ++k)
+            u += block_units<ROWS, OVER>(A, s, k);
+        int64_t upto = u;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int64_t up = __shfl_up_sync(0xffffffffu, upto, m);
+            if (lane >= m)
+                upto += up;
+        }
+        const bool here = off < upto && off >= upto - u;
+        int64_t at = upto - u;
+        if (here)
+#pragma unroll 1
+            for (i = i0; i < i1; ++i) {
+                const int k = block_units<ROWS, OVER>(A, s, i);
+                if (off < at + k)
+                    break;
+                at += k;
+            }
+        const int from = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+        i = __shfl_sync(0xffffffffu, i, from & 31);
+        t = __shfl_sync(0xffffffffu, (int)(off - at), from & 31);
+    }
+    int left = r.count;
+    int64_t unit = r.first;
+#pragma unroll 1
+    for (int k = 0;;) {
+        Seg q = {};
+        if (left > 0) {
+            int lo, hi;
+            block_keys<ROWS>(A, s, i, lo, hi);
+            const int all = hi / kTile - lo / kTile + 1, end = min(all + OVER, t + left);
+            const int t0 = max(0, t - OVER);
+            q.nt = max(0, end - OVER) - t0;
+            q.kt = lo / kTile + t0;
+            q.b = b, q.h = h, q.row0 = s.row0, q.n = s.n, q.first = s.L - s.n, q.lo = lo, q.hi = hi;
+            q.blk = i * ROWS;
+            q.tok0 = q.blk / B.G;
+            q.rem0 = q.blk - q.tok0 * B.G;
+            q.begins = t0 == 0;
+            q.whole = q.nt == all;
+            q.last_cta = share_of(r.total, r.n_cta, unit + (all + OVER - t) - 1);
+            left -= end - t;
+            unit += end - t;
+            t = 0;
+            if (left > 0 && ++i == n) {
+                i = 0;
+                if (++h == B.Hkv) {
+                    h = 0;
+                    do {
+                        if (++b >= B.n_seq) {   // not reached while the batch stays as it was counted
+                            left = 0;
+                            break;
+                        }
+                        s = load_seq(B, b);
+                        n = blocks_of<ROWS>(B, s);
+                    } while (n == 0);
+                }
+            }
+            if (q.nt == 0)   // the share ends ahead of the block's first tile
+                continue;
+        }
+        const int slot = k % kRing;
+        if (k >= kRing)
+            wait(ring.free[slot], (k / kRing - 1) & 1);
+        if (lane == 0) {
+            ring.seg[slot] = q;
+            tc::mbar_arrive(tc::smem_addr(&ring.full[slot]));
+        }
+        if (q.nt == 0)
+            return;
+        ++k;
+    }
+}
+
+// Segment k of the ring, for a whole warp; its slot is handed back at once.
+template <typename W>
+__device__ __forceinline__ Seg take_seg(Ring &ring, int k, W wait)
+{
+    const int slot = k % kRing;
+    wait(ring.full[slot], (k / kRing) & 1);
+    const Seg q = ring.seg[slot];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        tc::mbar_arrive(tc::smem_addr(&ring.free[slot]));
+    return q;
+}
+
+// Sequences without keys: nobody else looks at them. Their rows are zero, and bad entries are reported.
+template <int ROWS>
+__device__ __forceinline__ void clear_empty(const AttnArgs &A, int *error)
+{
+    const Batch &B = A.b;
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int b = blockIdx.x; b < B.n_seq; b += gridDim.x) {
+        const Seq s = load_seq(B, b);
+        if (!s.ok && lane == 0)
+            atomicOr(error, kErrMeta);
+        if (s.ok && s.L == 0) {
+            uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(A.out) + (int64_t)s.row0 * B.Hq * kHd * 2);
+            for (int64_t e = lane; e < (int64_t)s.n * B.Hq * (kHd / 8); e += 32)
+                o[e] = make_uint4(0, 0, 0, 0);
+        }
+    }
+}
+
+}  // namespace attn
+}  // namespace gdn

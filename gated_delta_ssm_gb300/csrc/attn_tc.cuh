@@ -7,17 +7,15 @@
 #include <cuda_fp8.h>
 #include <math_constants.h>
 
-#include "attn_device.cuh"
+#include "attn_share.cuh"
 #include "tc_ptx.cuh"
 #include "tma_map.cuh"
 
 namespace gdn {
 namespace attn {
 
-constexpr int kTile = 128;                    // keys per tile
 constexpr uint32_t kTileBytes = kTile * kHd;  // one tile of K or V codes
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kNoWindow = 1 << 30;            // positions are below this
 
 // D[tmem] (+)= A[smem] * B[smem]^T with e4m3 operands and 32-bit sums (a K step is 32).
 __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
@@ -49,13 +47,6 @@ __device__ __forceinline__ float redux_max(float x)
     float y;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
     return y;
-}
-
-// The batch's tiles shared out over n CTAs: share c begins at unit total * c / n.
-__device__ __forceinline__ int64_t share_begin(int64_t total, int n, int c) { return total * c / n; }
-__device__ __forceinline__ int share_of(int64_t total, int n, int64_t unit)
-{
-    return (int)(((unit + 1) * n - 1) / total);
 }
 
 // Two e4m3 numbers whose sum is (x, y) to within 2^-8 of each, down to steps of 2^-9: the low byte of
