@@ -48,6 +48,11 @@ constexpr uint32_t kTmemCols = 512;           // S of A, S of B, O of A, O of B:
 // numbers of 8 exponent bits, so a reference that lags behind costs no precision, only range.
 constexpr float kSlack = 8.0f, kSlackSum = 65536.0f;   // 128 weights of at most 2^8 sum to 2^15
 
+// How scores are capped: not, so low that weights need no reference, or anyhow.
+enum { kNoCap = 0, kLowCap = 1, kAnyCap = 2 };
+// In base 2: sums of 2^30 weights stay below 2^110; and the factor 2 log2 e / cap stays finite.
+constexpr float kMostCap = 80.0f, kLeastCap = 1e-6f;
+
 struct Shared {
     uint64_t k_full[kKs], k_free[kKs], v_full[kVs], v_free[kVs], b_full[kVb], b_free[kVb];
     uint64_t q_full[2], s_full[2], p_full[2], o_done[2], drain[2];
@@ -112,10 +117,10 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
     return d;
 }
 
-template <bool CAP>
+template <int CAP>
 __device__ __forceinline__ float score(float s, float fk, float cap2, float inv_cap2)
 {
-    if constexpr (CAP)
+    if constexpr (CAP != kNoCap)
         return cap2 * tanh_cap(s * fk * inv_cap2);
     else
         return s * fk;
@@ -133,6 +138,18 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 __device__ __forceinline__ uint64_t pack2(float lo, float hi)
 {
@@ -169,9 +186,8 @@ __device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16])
 // Weights of a row that sees the whole tile, against the reference as it is: one pass, no maximum. They are
 // stored if every row of the warp stayed within 2^kSlack summed; otherwise the scores are left as they were
 // and the caller takes the form that moves the reference.
-template <bool CAP, typename F>
-__device__ __forceinline__ bool row_weights_once(uint32_t s_at, F factor, float ref, float &l, float cap2,
-                                                 float inv_cap2)
+template <typename F>
+__device__ __forceinline__ bool row_weights_once(uint32_t s_at, F factor, float ref, float &l)
 {
     uint32_t x[2][16], y[64];
     uint64_t sum[2] = {0, 0};
@@ -188,13 +204,7 @@ __device__ __forceinline__ bool row_weights_once(uint32_t s_at, F factor, float 
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
             const float s0 = __uint_as_float(v[e]), s1 = __uint_as_float(v[e + 1]);
-            float2 z;
-            if constexpr (CAP) {
-                z.x = score<CAP>(s0, fk, cap2, inv_cap2) - ref;
-                z.y = score<CAP>(s1, fk, cap2, inv_cap2) - ref;
-            } else {
-                z = unpack2(fma2(pack2(s0, s1), fk2, sub2));
-            }
+            float2 z = unpack2(fma2(pack2(s0, s1), fk2, sub2));
             z.x = ex2(z.x);
             z.y = ex2(z.y);
             sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pack2(z.x, z.y));
@@ -212,6 +222,54 @@ __device__ __forceinline__ bool row_weights_once(uint32_t s_at, F factor, float 
     return true;
 }
 
+// Weights of a row whose scores are capped at no more than kMostCap: the weights themselves stay within the
+// range of the numbers that hold them, so no reference is needed, and no maximum. In base 2 the capped score is
+// c - 2 c / (1 + e^(2 s / cap)); its absolute error, c 2^-22, is far below a bf16 weight's rounding. One
+// reciprocal serves two keys: exponents are held to 60, where tanh is 1.
+template <bool WHOLE, typename M, typename F>
+__device__ __forceinline__ float row_weights_capped(uint32_t s_at, M mask_of, F factor, float c)
+{
+    uint64_t sum[2] = {0, 0};
+    const uint64_t one = pack2(1.0f, 1.0f), c2 = pack2(c, c), m2c = pack2(-2.0f * c, -2.0f * c);
+    const float f = 2.0f * kLog2e / c;    // factor() gives base-2 scores: 2 log2 e s / cap = (2 log2 e / c) (s log2 e)
+#pragma unroll 1
+    for (int q4 = 0; q4 < 4; ++q4) {
+        uint32_t v[32], y[16];
+        tmem_get32(s_at + 32 * q4, v);
+        tmem_wait32(v);
+        const uint32_t mask = WHOLE ? 0xffffffffu : mask_of(q4);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const float fk = factor(2 * q4 + half) * f;
+            const uint64_t fk2 = pack2(fk, fk);
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+                const int i = 16 * half + e;
+                float2 a = make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                if (!WHOLE) {   // columns that are not seen may hold NaN, and pairs share a reciprocal
+                    a.x = mask >> i & 1 ? a.x : 0.0f;
+                    a.y = mask >> (i + 1) & 1 ? a.y : 0.0f;
+                }
+                a = unpack2(mul2(pack2(a.x, a.y), fk2));
+                a = unpack2(add2(pack2(ex2(fminf(a.x, 60.0f)), ex2(fminf(a.y, 60.0f))), one));
+                const float r = rcp(a.x * a.y);
+                const float2 w = unpack2(fma2(mul2(pack2(r, r), pack2(a.y, a.x)), m2c, c2));
+                float2 z = make_float2(ex2(w.x), ex2(w.y));
+                if (!WHOLE) {
+                    z.x = mask >> i & 1 ? z.x : 0.0f;
+                    z.y = mask >> (i + 1) & 1 ? z.y : 0.0f;
+                }
+                const uint64_t z2 = pack2(z.x, z.y);
+                sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], z2);
+                y[8 * half + e / 2] = pack_bf16x2(z.x, z.y);
+            }
+        }
+        tc::tmem_st16u(s_at + 16 * q4, y);
+    }
+    const float2 t = unpack2(add2(sum[0], sum[1]));
+    return t.x + t.y;
+}
+
 // 16 bytes to shared memory without passing through registers; zeros where `have` is false.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool have)
 {
@@ -221,7 +279,7 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool have)
 
 // The largest visible score of this thread's row of the tile (128 columns at s_at), -inf for none. The cap
 // is monotonic and factors are not negative, so each 16 columns' raw maximum stands for them.
-template <bool CAP, typename M, typename F>
+template <int CAP, typename M, typename F>
 __device__ __forceinline__ float row_max(uint32_t s_at, M mask_of, F factor, float cap2, float inv_cap2)
 {
     float top = -INFINITY;
@@ -249,7 +307,7 @@ __device__ __forceinline__ float row_max(uint32_t s_at, M mask_of, F factor, flo
 
 // Weights of the row, 2^(score - sub), as bf16 pairs over the scores' columns; returns their sum. Weights
 // of 32 keys take 16 columns, over scores already read.
-template <bool CAP, typename M, typename F>
+template <int CAP, typename M, typename F>
 __device__ __forceinline__ float row_weights(uint32_t s_at, M mask_of, F factor, float sub, float cap2,
                                              float inv_cap2)
 {
@@ -281,7 +339,7 @@ __device__ __forceinline__ float row_weights(uint32_t s_at, M mask_of, F factor,
     return sum;
 }
 
-template <bool CAP>
+template <int CAP>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ CUtensorMap map_k,
                     const __grid_constant__ CUtensorMap map_v)
@@ -472,7 +530,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
         const uint32_t s_at = tmem + m * 128 + lane_at, o_at = tmem + 256 + m * 128 + lane_at;
         const int per_tile = kTile >> page_shift;
         const int G = B.G, inv_G = 65536 / G + 1;   // y / G = y * inv_G >> 16 for y below 4096
-        const float cap2 = A.softcap * kLog2e, inv_cap2 = CAP ? 1.0f / cap2 : 0.0f;
+        const float cap2 = A.softcap * kLog2e, inv_cap2 = CAP == kAnyCap ? 1.0f / cap2 : 0.0f;
         const float f_scale = fabsf(A.scale) * kLog2e, sign = A.scale < 0.0f ? -1.0f : 1.0f;
         int c = 0;
         // the segment whose rows are written next
@@ -593,7 +651,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
             int p_far = page_at(1);
             float ks_next = scale_at(page_at(0));
             const float f = sh.f[m][row];
-            ref = -INFINITY;
+            ref = CAP == kLowCap ? 0.0f : -INFINITY;
             l = 0.0f;
 #pragma unroll 1
             for (int t = 0; t < w.nt; ++t, ++c) {
@@ -608,44 +666,49 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                 };
                 wait(sh.s_full[m], c & 1);
                 tc::fence_after_sync();
-                if (!whole || !__all_sync(0xffffffffu, ref > -INFINITY) ||
-                    !row_weights_once<CAP>(s_at, factor, ref, l, cap2, inv_cap2)) {
-                    const int hi = limit - j0, lo = limit - A.window + 1 - j0;   // visible columns [lo, hi]
-                    // bit e: column 32 q4 + e is visible
-                    auto mask_of = [&](int q4) {
-                        const int h = hi - 32 * q4, o = lo - 32 * q4;
-                        uint32_t v = h >= 31 ? 0xffffffffu : h < 0 ? 0u : (2u << h) - 1u;
-                        v &= o <= 0 ? 0xffffffffu : o > 31 ? 0u : 0xffffffffu << o;
-                        if (bad >> ((32 * q4) >> page_shift) & 1)
-                            v &= 0xffff0000u;
-                        if (bad >> ((32 * q4 + 16) >> page_shift) & 1)
-                            v &= 0x0000ffffu;
-                        return v;
-                    };
-                    const float top = row_max<CAP>(s_at, mask_of, factor, cap2, inv_cap2);
-                    // the reference moves when a weight would pass 2^kSlack, or is the row's first
-                    const bool move = top > ref + kSlack || (ref == -INFINITY && top > ref);
-                    if (__any_sync(0xffffffffu, move)) {
-                        const float to = move ? top : ref;
-                        const float a = move ? ex2(ref - to) : 1.0f;
-                        ref = to;
-                        l *= a;
-                        if (t > 0) {
-                            wait(sh.o_done[m], (c - 1) & 1);
-                            tc::fence_after_sync();
+                const int hi = limit - j0, lo = limit - A.window + 1 - j0;   // visible columns [lo, hi]
+                // bit e: column 32 q4 + e is visible
+                auto mask_of = [&](int q4) {
+                    const int h = hi - 32 * q4, o = lo - 32 * q4;
+                    uint32_t v = h >= 31 ? 0xffffffffu : h < 0 ? 0u : (2u << h) - 1u;
+                    v &= o <= 0 ? 0xffffffffu : o > 31 ? 0u : 0xffffffffu << o;
+                    if (bad >> ((32 * q4) >> page_shift) & 1)
+                        v &= 0xffff0000u;
+                    if (bad >> ((32 * q4 + 16) >> page_shift) & 1)
+                        v &= 0x0000ffffu;
+                    return v;
+                };
+                if constexpr (CAP == kLowCap) {
+                    l += whole ? row_weights_capped<true>(s_at, mask_of, factor, cap2)
+                               : row_weights_capped<false>(s_at, mask_of, factor, cap2);
+                } else {
+                    if (CAP == kAnyCap || !whole || !__all_sync(0xffffffffu, ref > -INFINITY) ||
+                        !row_weights_once(s_at, factor, ref, l)) {
+                        const float top = row_max<CAP>(s_at, mask_of, factor, cap2, inv_cap2);
+                        // the reference moves when a weight would pass 2^kSlack, or is the row's first
+                        const bool move = top > ref + kSlack || (ref == -INFINITY && top > ref);
+                        if (__any_sync(0xffffffffu, move)) {
+                            const float to = move ? top : ref;
+                            const float a = move ? ex2(ref - to) : 1.0f;
+                            ref = to;
+                            l *= a;
+                            if (t > 0) {
+                                wait(sh.o_done[m], (c - 1) & 1);
+                                tc::fence_after_sync();
 #pragma unroll 1
-                            for (int q4 = 0; q4 < 8; ++q4) {
-                                uint32_t v[16];
-                                tmem_get16(o_at + 16 * q4, v);
-                                tmem_wait16(v);
+                                for (int q4 = 0; q4 < 8; ++q4) {
+                                    uint32_t v[16];
+                                    tmem_get16(o_at + 16 * q4, v);
+                                    tmem_wait16(v);
 #pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    v[e] = __float_as_uint(__uint_as_float(v[e]) * a);
-                                tc::tmem_st16u(o_at + 16 * q4, v);
+                                    for (int e = 0; e < 16; ++e)
+                                        v[e] = __float_as_uint(__uint_as_float(v[e]) * a);
+                                    tc::tmem_st16u(o_at + 16 * q4, v);
+                                }
                             }
                         }
+                        l += row_weights<CAP>(s_at, mask_of, factor, ref == -INFINITY ? 0.0f : ref, cap2, inv_cap2);
                     }
-                    l += row_weights<CAP>(s_at, mask_of, factor, ref == -INFINITY ? 0.0f : ref, cap2, inv_cap2);
                 }
                 tc::tmem_wait_st();
                 tc::fence_before_sync();
@@ -692,28 +755,36 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                 wait(sh.v_full[vst], (c / kVs) & 1);
                 const uint8_t *src = mem + kVAt + vst * kTileBytes + t128 * kHd;
                 uint8_t *dst = mem + kBAt + vb * 2 * kTileBytes + (t128 >> 3) * 1024 + (t128 & 7) * 128;
-#pragma unroll 2
-                for (int i = 0; i < 8; ++i) {
-                    const uint4 raw = dead ? make_uint4(0, 0, 0, 0)
-                                           : *reinterpret_cast<const uint4 *>(src + ((i ^ (t128 & 7)) << 4));
-                    const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-                    uint32_t o[8];
+                // four 16-byte pieces in flight at a time: one warp per scheduler does this, so its own
+                // independent work is all that hides its latencies
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    uint4 raw[4];
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        o[2 * z] = mul_bf16x2(codes_bf16(__byte_perm(in[z], 0, 0x1404)), f1);
-                        o[2 * z + 1] = mul_bf16x2(codes_bf16(__byte_perm(in[z], 0, 0x3424)), f1);
-                    }
-                    if (e2 != 0) {
+                    for (int i = 0; i < 4; ++i)
+                        raw[i] = *reinterpret_cast<const uint4 *>(src + (((4 * half + i) ^ (t128 & 7)) << 4));
+                    uint8_t *const to = dst + half * kTileBytes;
 #pragma unroll
-                        for (int z = 0; z < 8; ++z)
-                            o[z] = mul_bf16x2(o[z], f2);
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t in[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                        uint32_t o[8];
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const uint32_t code = dead ? 0u : in[z];
+                            o[2 * z] = mul_bf16x2(codes_bf16(__byte_perm(code, 0, 0x1404)), f1);
+                            o[2 * z + 1] = mul_bf16x2(codes_bf16(__byte_perm(code, 0, 0x3424)), f1);
+                        }
+                        if (e2 != 0) {
+#pragma unroll
+                            for (int z = 0; z < 8; ++z)
+                                o[z] = mul_bf16x2(o[z], f2);
+                        }
+                        // dimensions 16 (4 half + i) ..: two 16-byte pieces
+                        *reinterpret_cast<uint4 *>(to + (((2 * i) ^ (t128 & 7)) << 4)) =
+                            make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4 *>(to + (((2 * i + 1) ^ (t128 & 7)) << 4)) =
+                            make_uint4(o[4], o[5], o[6], o[7]);
                     }
-                    // dimensions 16 i .. 16 i + 15: two 16-byte pieces of half i / 4
-                    uint8_t *half = dst + (i >> 2) * kTileBytes;
-                    const int p0 = (2 * i) & 7;
-                    *reinterpret_cast<uint4 *>(half + ((p0 ^ (t128 & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4 *>(half + (((p0 + 1) ^ (t128 & 7)) << 4)) =
-                        make_uint4(o[4], o[5], o[6], o[7]);
                 }
                 arrive(sh.v_free[vst]);
                 tc::fence_smem_to_async();
@@ -730,7 +801,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
         tc::tmem_dealloc(tmem, kTmemCols);
 }
 
-template <bool CAP>
+template <int CAP>
 cudaError_t launch_cap(const AttnArgs &a, int grid, cudaStream_t s)
 {
     CUtensorMap mk, mv;
@@ -769,7 +840,9 @@ cudaError_t launch_prefill(const AttnArgs &args, cudaStream_t s)
     const int64_t blocks = ((int64_t)b.max_q * b.G + kRows - 1) / kRows * b.Hkv * b.n_seq;
     const int grid = (int)(tiles >= a.sm_count || blocks >= a.sm_count || tiles * blocks >= a.sm_count
                                ? a.sm_count : tiles * blocks);
-    return a.softcap > 0.0f ? launch_cap<true>(a, grid, s) : launch_cap<false>(a, grid, s);
+    if (a.softcap == 0.0f)
+        return launch_cap<kNoCap>(a, grid, s);
+    return a.softcap * kLog2e <= kMostCap && a.softcap >= kLeastCap ? launch_cap<kLowCap>(a, grid, s) : launch_cap<kAnyCap>(a, grid, s);
 }
 
 cudaError_t take_prefill_error(int *code)
