@@ -63,13 +63,6 @@ struct Shared {
     float f[2][128];           // |scale| log2 e / (power of two of the q row)
 };
 
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
-
 // 32 columns of this thread's lane, without waiting; tmem_wait makes them usable.
 __device__ __forceinline__ void tmem_get32(uint32_t taddr, uint32_t (&r)[32])
 {
@@ -522,7 +515,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
         __syncwarp();
     } else if (warp == 3) {
         walk_share<kThreads, kRows, kOver>(A, sh.share, share, sh.ring, wait);
-        clear_empty<kRows>(A, &g_attn_prefill_error);
+        clear_empty(A, &g_attn_prefill_error);
     } else if (warp < 12) {
         // ------------------------------------------------------------ scores to weights: a row per thread
         const int m = (warp - 4) >> 2, row = (tid - 128) & 127, x = m * 128 + row;
@@ -838,8 +831,8 @@ cudaError_t launch_prefill(const AttnArgs &args, cudaStream_t s)
         a.window = kNoWindow;
     const int64_t tiles = ((int64_t)b.max_pages * b.P + kTile - 1) / kTile;
     const int64_t blocks = ((int64_t)b.max_q * b.G + kRows - 1) / kRows * b.Hkv * b.n_seq;
-    const int grid = (int)(tiles >= a.sm_count || blocks >= a.sm_count || tiles * blocks >= a.sm_count
-                               ? a.sm_count : tiles * blocks);
+    const int64_t units = tiles >= a.sm_count || blocks >= a.sm_count ? a.sm_count : (tiles + kOver) * blocks;
+    const int grid = (int)(units < a.sm_count ? units : a.sm_count);
     if (a.softcap == 0.0f)
         return launch_cap<kNoCap>(a, grid, s);
     return a.softcap * kLog2e <= kMostCap && a.softcap >= kLeastCap ? launch_cap<kLowCap>(a, grid, s) : launch_cap<kAnyCap>(a, grid, s);

@@ -258,7 +258,6 @@ __device__ __forceinline__ Seg take_seg(Ring &ring, int k, W wait)
 }
 
 // Sequences without keys: nobody else looks at them. Their rows are zero, and bad entries are reported.
-template <int ROWS>
 __device__ __forceinline__ void clear_empty(const AttnArgs &A, int *error)
 {
     const Batch &B = A.b;

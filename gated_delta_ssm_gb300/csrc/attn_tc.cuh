@@ -30,6 +30,13 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) { return tc::idesc_f16(M, N); }
 constexpr uint32_t kIdescTransA = 1u << 15;   // A is MN-major
 
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
