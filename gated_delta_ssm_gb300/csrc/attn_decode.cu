@@ -41,16 +41,18 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kOver = 1;     // what a block costs besides its tiles, in tiles
+constexpr float kNoRef = -1e30f;   // below every reference, and finite: 2^(-inf - kNoRef) is 0
 
 template <int NR>            // rows, padded
 struct Cfg {
     // tiles in flight, K and V counted apart (item 2 i is K of tile i, 2 i + 1 its V)
-    static constexpr int kItems = NR == 16 ? 5 : NR == 32 ? 10 : 8;
+    static constexpr int kItems = NR == 16 ? 5 : NR == 32 ? 8 : 6;
     static constexpr int kCtas = NR == 16 ? 2 : 1;               // CTAs per SM
     static constexpr uint32_t kRowBytes = NR * kHd;              // one e4m3 operand of NR rows
     static constexpr uint32_t kQ = kItems * kTileBytes;          // [2 segments][hi, lo]
     static constexpr uint32_t kP = kQ + 4 * kRowBytes;           // [2 tiles][hi, lo]
-    static constexpr uint32_t kEnd = kP + 4 * kRowBytes;
+    static constexpr uint32_t kO32 = kP + 4 * kRowBytes;         // a segment's joined products, float [NR][128]
+    static constexpr uint32_t kEnd = kO32 + 4 * kRowBytes;
     // tensor memory: S of two tiles, then the four warps' products of kO tiles
     static constexpr int kO = NR == 64 ? 1 : 2;
     static constexpr uint32_t kTmemCols = NR == 16 ? 256 : 512;
@@ -69,6 +71,7 @@ struct Shared {
     float f[2][NR];            // scale * log2 e / (power of two of the q row)
     int limit[2][NR];          // position of each row
     float l_sum[2][4][NR], l_ref[2][4][NR];
+    float o_ref[NR];
 };
 
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8])
@@ -85,21 +88,17 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8])
         v[i] = __uint_as_float(r[i]);
 }
 
-// 8 columns of each of the four warps' products, `step` columns apart.
-__device__ __forceinline__ void tmem_ld4x8(uint32_t taddr, uint32_t step, uint32_t (&r)[4][8])
+// 4 columns of each of the four warps' products, `step` columns apart.
+__device__ __forceinline__ void tmem_ld4x4(uint32_t taddr, uint32_t step, uint32_t (&r)[4][4])
 {
 #pragma unroll
     for (int w = 0; w < 4; ++w)
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                     : "=r"(r[w][0]), "=r"(r[w][1]), "=r"(r[w][2]), "=r"(r[w][3]), "=r"(r[w][4]), "=r"(r[w][5]),
-                       "=r"(r[w][6]), "=r"(r[w][7])
-                     : "r"(taddr + w * step));
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[w][0]), "=r"(r[w][1]), "=r"(r[w][2]), "=r"(r[w][3]) : "r"(taddr + w * step));
 #pragma unroll
     for (int w = 0; w < 4; ++w)
         asm volatile("tcgen05.wait::ld.sync.aligned;"
-                     : "+r"(r[w][0]), "+r"(r[w][1]), "+r"(r[w][2]), "+r"(r[w][3]), "+r"(r[w][4]), "+r"(r[w][5]),
-                       "+r"(r[w][6]), "+r"(r[w][7])
-                     :: "memory");
+                     : "+r"(r[w][0]), "+r"(r[w][1]), "+r"(r[w][2]), "+r"(r[w][3]) :: "memory");
 }
 
 // Sums over the warp of eight values per lane: lane i gets that of value i & 7. Halving the values each lane
@@ -169,18 +168,21 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
     tc::fence_smem_to_async();
 
     wait_previous_grid();
-    tc::fence_before_sync();
-    const Share share = find_share<kThreads, kMaxDecodeRows, kOver>(A, sh.share);
-    tc::fence_after_sync();
+    Share share = {};
+    if (B.n_seq > kFewSeqs)
+        share = find_share<kMaxDecodeRows, kOver>(A, sh.share, tid, kThreads, [] { __syncthreads(); });
     PartMeta *const meta = reinterpret_cast<PartMeta *>(A.ws);
     float *const parts = part_slots(A.ws, gridDim.x);
     if (tid == 256)   // the thread that may describe a block later
         meta[blockIdx.x].owner = 0;
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
     allow_next_grid();
 
     const uint32_t tmem = sh.tmem;
     const uint64_t lim = A.wait_ns;
-    const int page_shift = 31 - __clz(B.P);
+    const int page_shift = 31 - __clz(B.P), inv_G = 65536 / B.G + 1;   // r / G = r * inv_G >> 16 for r below 4096
     bool failed = false;
     // A wait that gives up stops the CTA's copies and products and ends every other wait; the loops
     // run on to their ends. wait is for whole warps.
@@ -321,7 +323,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
                 wait(sh.q_free[par], (k / 2 - 1) & 1);
 #pragma unroll 2
             for (int r = r4; r < NR; r += 4) {
-                const int tok = r / B.G, g = r - tok * B.G;
+                const int tok = r * inv_G >> 16, g = r - tok * B.G;
                 const bool live = tok < w.n;
                 float v[16] = {};
                 if (live)
@@ -347,7 +349,9 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
             arrive(sh.q_full[par]);
         }
     } else if (warp == 3) {
-        walk_share<kThreads, kMaxDecodeRows, kOver>(A, sh.share, share, sh.ring, wait);
+        if (B.n_seq <= kFewSeqs)
+            share = find_share<kMaxDecodeRows, kOver>(A, sh.share, lane, 32, [] { __syncwarp(); });
+        walk_share<kMaxDecodeRows, kOver>(A, share, sh.ring, wait);
         clear_empty(A, &g_attn_decode_error);
     } else if (warp < 8) {
         // ------------------------------------------------------------ scores to weights: a key per thread
@@ -497,66 +501,96 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
             if (w.nt == 0)
                 break;
             const int par_q = k & 1;
-            float o[NR], ref[NR];      // O of row r is o 2^ref
+            float o[NR];               // O of row r is o 2^o_ref[r]
 #pragma unroll
             for (int r = 0; r < NR; ++r)
-                o[r] = 0.0f, ref[r] = -INFINITY;
+                o[r] = 0.0f;
+            named_sync(1, 128);        // the last segment's rows are out
+            if (d < NR)
+                sh.o_ref[d] = kNoRef;
+            named_sync(1, 128);
 #pragma unroll 1
             for (int t = 0; t < w.nt; ++t, ++i) {
                 const int ob = i % C::kO;
                 wait(sh.coef_full[i & 3], (i >> 2) & 1);
+                // the references lag: sums of 32 bits do not mind 2^60
+                bool move = false;
+                if (lane < R) {
+#pragma unroll
+                    for (int e = 0; e < C::kLs; ++e) {
+                        const float4 m = sh.top[i & 3][32 * e + lane < R ? 32 * e + lane : lane];
+                        move |= fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)) >
+                                sh.o_ref[32 * e + lane < R ? 32 * e + lane : lane] + 60.0f;
+                    }
+                }
+                if (__any_sync(0xffffffffu, move)) {   // the same in all four warps
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) {
+                        if (r % 4 == 0 && r >= R)
+                            break;
+                        const float4 m = sh.top[i & 3][r];
+                        const float ref = sh.o_ref[r];
+                        o[r] *= ex2(ref - fmaxf(ref, fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w))));
+                    }
+                    named_sync(1, 128);
+                    if (d < R) {
+                        const float4 m = sh.top[i & 3][d];
+                        sh.o_ref[d] = fmaxf(sh.o_ref[d], fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)));
+                    }
+                    named_sync(1, 128);
+                }
                 wait(sh.o_full[ob], (i / C::kO) & 1);
                 tc::fence_after_sync();
 #pragma unroll
-                for (int c = 0; c < NR / 8; ++c) {
-                    if (c >= chunks)
+                for (int c = 0; c < NR / 4; ++c) {
+                    if (4 * c >= R)
                         break;
-                    uint32_t x[4][8];
-                    tmem_ld4x8(o_at + 4 * ob * NR + 8 * c, NR, x);
+                    uint32_t x[4][4];
+                    tmem_ld4x4(o_at + 4 * ob * NR + 4 * c, NR, x);
+                    const float4 refs = *reinterpret_cast<const float4 *>(&sh.o_ref[4 * c]);
+                    const float ref[4] = {refs.x, refs.y, refs.z, refs.w};
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int r = 8 * c + e;
+                    for (int e = 0; e < 4; ++e) {
+                        const int r = 4 * c + e;
                         const float4 m = sh.top[i & 3][r];
-                        // the reference lags: sums of 32 bits do not mind 2^60
-                        const float most = fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w));
-                        if (most > ref[r] + 60.0f || ref[r] == -INFINITY) {
-                            o[r] *= ref[r] == -INFINITY ? 0.0f : ex2(ref[r] - most);
-                            ref[r] = most;
-                        }
-                        const float sub = ref[r] == -INFINITY ? 0.0f : ref[r];
-                        o[r] = fmaf(__uint_as_float(x[0][e]), ex2(m.x - sub), o[r]);
-                        o[r] = fmaf(__uint_as_float(x[1][e]), ex2(m.y - sub), o[r]);
-                        o[r] = fmaf(__uint_as_float(x[2][e]), ex2(m.z - sub), o[r]);
-                        o[r] = fmaf(__uint_as_float(x[3][e]), ex2(m.w - sub), o[r]);
+                        o[r] = fmaf(__uint_as_float(x[0][e]), ex2(m.x - ref[e]), o[r]);
+                        o[r] = fmaf(__uint_as_float(x[1][e]), ex2(m.y - ref[e]), o[r]);
+                        o[r] = fmaf(__uint_as_float(x[2][e]), ex2(m.z - ref[e]), o[r]);
+                        o[r] = fmaf(__uint_as_float(x[3][e]), ex2(m.w - ref[e]), o[r]);
                     }
                 }
                 tc::fence_before_sync();
                 arrive(sh.o_free[ob]);
             }
+            // through shared memory, so that a warp writes whole rows and the code does not know their number
+            float *const stage = reinterpret_cast<float *>(mem + C::kO32);
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+                stage[r * kHd + d] = o[r];
+            named_sync(1, 128);
             wait(sh.l_full[par_q], (k >> 1) & 1);
             const int rows = w.n * B.G;
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(A.out) +
-                                 ((int64_t)w.row0 * B.Hq + (int64_t)w.h * B.G) * kHd + d;
             float *part = parts + (size_t)(2 * blockIdx.x + (w.begins ? 1 : 0)) * R * kPartRow;
-#pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                if (r >= rows)
-                    break;
+#pragma unroll 1
+            for (int r = wq; r < rows; r += 4) {
+                const float at = sh.o_ref[r];
                 float l = 0.0f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float by = sh.l_ref[par_q][e][r];
-                    // a warp without visible keys adds its sum as it is: zero, or NaN
-                    l += sh.l_sum[par_q][e][r] * (by == -INFINITY ? 1.0f : ex2(by - ref[r]));
-                }
+                for (int e = 0; e < 4; ++e)
+                    l += sh.l_sum[par_q][e][r] * ex2(sh.l_ref[par_q][e][r] - at);
+                const float4 x = *reinterpret_cast<const float4 *>(stage + r * kHd + 4 * lane);
                 if (w.whole) {
-                    const int tok = r / B.G, g = r - tok * B.G;
-                    out[((int64_t)tok * B.Hq + g) * kHd] =
-                        __float2bfloat16_rn(l > 0.0f ? o[r] / l : (l == l ? 0.0f : l));
+                    const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
+                    const int tok = r * inv_G >> 16, g = r - tok * B.G;
+                    const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x * inv, x.y * inv);
+                    const __nv_bfloat162 hi = __floats2bfloat162_rn(x.z * inv, x.w * inv);
+                    reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(A.out) +
+                                              ((int64_t)(w.row0 + tok) * B.Hq + w.h * B.G + g) * kHd)[lane] =
+                        make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
                 } else {
-                    part[r * kPartRow + d] = o[r];
-                    if (d == 0)
-                        *reinterpret_cast<float2 *>(part + r * kPartRow + kHd) = make_float2(l, ref[r]);
+                    *reinterpret_cast<float4 *>(part + r * kPartRow + 4 * lane) = x;
+                    if (lane == 0)
+                        *reinterpret_cast<float2 *>(part + r * kPartRow + kHd) = make_float2(l, at);
                 }
             }
             if (!w.whole && w.begins && d == 0)

@@ -10,10 +10,15 @@ namespace gdn {
 namespace attn {
 
 // CTA x joins the block that begins in share x: its own part (slot 2 x + 1) and the parts that the shares
-// after it began with (slots 2 c). A warp per row, four dimensions per lane. A part's row holds the 128
-// unnormalised sums, the sum of weights l and their reference m: the true values are 2^m times these.
+// after it began with (slots 2 c). A part's row holds the 128 unnormalised sums, the sum of weights l and their
+// reference m: the true values are 2^m times these. SPLIT warps take a row's parts in turn, four dimensions per
+// lane: all maxima are read first (a lane per part), so the sums' loads do not wait for one another.
+template <int SPLIT>
 __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnArgs A, int rows)
 {
+    constexpr int kPerCta = 4 / SPLIT;
+    __shared__ float4 sum[4][32];
+    __shared__ float sum_l[4];
     const Batch &B = A.b;
     wait_previous_grid();
     allow_next_grid();
@@ -21,29 +26,51 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
     if (!m.owner)
         return;
     const Seq s = load_seq(B, m.b);
-    const int i = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int r = m.row0 + i;
-    if (i >= rows || r >= s.n * B.G)
-        return;
-    const float *parts = part_slots(A.ws, gridDim.x);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int i = blockIdx.y * kPerCta + warp / SPLIT, piece = warp % SPLIT;
+    const int r = m.row0 + i, n = m.last_cta - (int)blockIdx.x + 1;
+    const bool live = i < rows && r < s.n * B.G;
     const size_t size = (size_t)rows * kPartRow;
-    float big = -INFINITY, l = 0.0f;
+    const float *own = part_slots(A.ws, gridDim.x) + (size_t)(2 * blockIdx.x) * size + (size_t)i * kPartRow;
+    auto part = [&](int c) { return own + (size_t)(c == 0 ? 1 : 2 * c) * size; };
+    float l = 0.0f;
     float4 o = make_float4(0, 0, 0, 0);
+    if (live) {
+        float big = -INFINITY;
+        for (int c = lane; c < n; c += 32)
+            big = fmaxf(big, part(c)[kHd + 1]);
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1)
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, k));
 #pragma unroll 4
-    for (int c = blockIdx.x; c <= m.last_cta; ++c) {
-        const float *p = parts + (size_t)(2 * c + (c == (int)blockIdx.x ? 1 : 0)) * size + (size_t)i * kPartRow;
-        const float2 lm = *reinterpret_cast<const float2 *>(p + kHd);
-        const float4 x = *reinterpret_cast<const float4 *>(p + 4 * lane);
-        const float grown = fmaxf(big, lm.y);
-        const float a = grown == -INFINITY ? 1.0f : exp2f(big - grown);
-        const float b = grown == -INFINITY ? 0.0f : exp2f(lm.y - grown);
-        l = fmaf(l, a, lm.x * b);
-        o.x = fmaf(o.x, a, x.x * b);
-        o.y = fmaf(o.y, a, x.y * b);
-        o.z = fmaf(o.z, a, x.z * b);
-        o.w = fmaf(o.w, a, x.w * b);
-        big = grown;
+        for (int c = piece; c < n; c += SPLIT) {
+            const float *p = part(c);
+            const float2 lm = *reinterpret_cast<const float2 *>(p + kHd);
+            const float4 x = *reinterpret_cast<const float4 *>(p + 4 * lane);
+            const float b = big == -INFINITY ? 0.0f : exp2f(lm.y - big);
+            l = fmaf(lm.x, b, l);
+            o.x = fmaf(x.x, b, o.x);
+            o.y = fmaf(x.y, b, o.y);
+            o.z = fmaf(x.z, b, o.z);
+            o.w = fmaf(x.w, b, o.w);
+        }
     }
+    if (SPLIT > 1) {
+        sum[warp][lane] = o;
+        if (lane == 0)
+            sum_l[warp] = l;
+        __syncthreads();
+        if (piece != 0)
+            return;
+#pragma unroll
+        for (int k = 1; k < SPLIT; ++k) {
+            const float4 x = sum[warp + k][lane];
+            l += sum_l[warp + k];
+            o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+        }
+    }
+    if (!live)
+        return;
     const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
     const int tok = r / B.G, g = r - tok * B.G;
     const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv);
@@ -53,18 +80,21 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
         make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
 }
 
+// A decode call's few rows can span every CTA, so four warps share a row; a prefill block has 256 rows of
+// two or three parts.
 cudaError_t launch_join(const AttnArgs &a, int grid, int rows, cudaStream_t s)
 {
+    const bool few = rows <= kMaxDecodeRows;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(grid, (rows + 3) / 4);
+    cfg.gridDim = dim3(grid, few ? rows : (rows + 3) / 4);
     cfg.blockDim = dim3(128);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel, a, rows);
+    return cudaLaunchKernelEx(&cfg, few ? attn_join_kernel<4> : attn_join_kernel<1>, a, rows);
 }
 
 }  // namespace attn

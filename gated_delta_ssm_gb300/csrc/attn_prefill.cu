@@ -367,13 +367,16 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
     if (warp == 1)
         tc::tmem_alloc(tc::smem_addr(&sh.tmem), kTmemCols);
     wait_previous_grid();
-    tc::fence_before_sync();
-    const Share share = find_share<kThreads, kRows, kOver>(A, sh.share);
-    tc::fence_after_sync();
+    Share share = {};
+    if (B.n_seq > kFewSeqs)
+        share = find_share<kRows, kOver>(A, sh.share, tid, kThreads, [] { __syncthreads(); });
     PartMeta *const meta = reinterpret_cast<PartMeta *>(A.ws);
     float *const parts = part_slots(A.ws, gridDim.x);
     if (tid == 128)   // the thread that may describe a block later
         meta[blockIdx.x].owner = 0;
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
     allow_next_grid();
 
     const uint32_t tmem = sh.tmem;
@@ -514,7 +517,9 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
         }
         __syncwarp();
     } else if (warp == 3) {
-        walk_share<kThreads, kRows, kOver>(A, sh.share, share, sh.ring, wait);
+        if (B.n_seq <= kFewSeqs)
+            share = find_share<kRows, kOver>(A, sh.share, lane, 32, [] { __syncwarp(); });
+        walk_share<kRows, kOver>(A, share, sh.ring, wait);
         clear_empty(A, &g_attn_prefill_error);
     } else if (warp < 12) {
         // ------------------------------------------------------------ scores to weights: a row per thread

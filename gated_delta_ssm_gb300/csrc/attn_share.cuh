@@ -37,9 +37,13 @@ struct Ring {
     uint64_t full[kRing], free[kRing];
 };
 
+// Batches of at most this many sequences are counted by the walking warp alone, larger ones by the whole CTA.
+constexpr int kFewSeqs = 256;
+
 template <int THREADS>
 struct ShareShared {
     int64_t warp_sum[THREADS / 32];
+    int64_t total;
     int64_t start_off, head_units;    // the share's first unit within its sequence; units of one KV head there
     int start_b;
 };
@@ -47,6 +51,8 @@ struct ShareShared {
 struct Share {
     int64_t total, first;             // units of the batch; the share's first
     int n_cta, count;                 // CTAs with a share; units of this one's
+    int b;                            // the first unit's sequence,
+    int64_t off, head_units;          // its place among that sequence's units, and those of one KV head
 };
 
 __device__ __forceinline__ int64_t share_begin(int64_t total, int n, int c) { return total * c / n; }
@@ -92,22 +98,24 @@ __device__ __forceinline__ int64_t head_units(const AttnArgs &A, int b, int from
     return u;
 }
 
-// Count the batch and find where this CTA's share begins. Every thread of the CTA calls it.
-template <int THREADS, int ROWS, int OVER>
-__device__ __forceinline__ Share find_share(const AttnArgs &A, ShareShared<THREADS> &sh)
+// Count the batch and find where this CTA's share begins, by `threads` threads of which this is number tid
+// (whole warps). sync joins them.
+template <int ROWS, int OVER, int THREADS, typename Y>
+__device__ __forceinline__ Share find_share(const AttnArgs &A, ShareShared<THREADS> &sh, int tid, int threads, Y sync)
 {
     const Batch &B = A.b;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int warp = tid >> 5, lane = tid & 31;
     // a group of g neighbouring lanes counts one sequence, or a thread several where there are many
     int g = 1;
-    while (g < 32 && (int64_t)B.n_seq * g * 2 <= THREADS)
+    while (g < 32 && B.n_seq * g * 2 <= threads)
         g *= 2;
-    const int per = g > 1 ? 1 : (B.n_seq + THREADS - 1) / THREADS;
+    const int per = g > 1 ? 1 : (B.n_seq + threads - 1) / threads;
     const int first_b = (tid / g) * per, sub = tid % g;
     int64_t mine = 0;
-#pragma unroll 1
-    for (int i = 0; i < per && first_b + i < B.n_seq; ++i)
-        mine += head_units<ROWS, OVER>(A, first_b + i, sub, g);
+#pragma unroll 2
+    for (int i = 0; i < per; ++i)
+        if (first_b + i < B.n_seq)
+            mine += head_units<ROWS, OVER>(A, first_b + i, sub, g);
     for (int m = 1; m < g; m <<= 1)
         mine += __shfl_xor_sync(0xffffffffu, mine, m);
     const int64_t one_head = mine;
@@ -119,15 +127,18 @@ __device__ __forceinline__ Share find_share(const AttnArgs &A, ShareShared<THREA
         if (lane >= m)
             incl += up;
     }
-    if (lane == 31)
-        sh.warp_sum[warp] = incl;
-    __syncthreads();
     Share r;
-    r.total = 0;
-#pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) {
-        incl += i < warp ? sh.warp_sum[i] : 0;
-        r.total += sh.warp_sum[i];
+    r.total = __shfl_sync(0xffffffffu, incl, 31);
+    if (threads > 32) {
+        if (lane == 31)
+            sh.warp_sum[warp] = incl;
+        sync();
+        r.total = 0;
+#pragma unroll 1
+        for (int i = 0; i < threads / 32; ++i) {
+            incl += i < warp ? sh.warp_sum[i] : 0;
+            r.total += sh.warp_sum[i];
+        }
     }
     r.n_cta = (int)min((int64_t)gridDim.x, r.total);
     const bool works = (int)blockIdx.x < r.n_cta;
@@ -147,25 +158,27 @@ __device__ __forceinline__ Share find_share(const AttnArgs &A, ShareShared<THREA
             at += u * B.Hkv;
         }
     }
-    __syncthreads();
+    sync();
+    r.b = sh.start_b;
+    r.off = sh.start_off;
+    r.head_units = sh.head_units;
     return r;
 }
 
 // One warp walks the share and fills the ring; `wait` is the kernel's bounded wait.
-template <int THREADS, int ROWS, int OVER, typename W>
-__device__ __forceinline__ void walk_share(const AttnArgs &A, const ShareShared<THREADS> &sh, const Share &r,
-                                           Ring &ring, W wait)
+template <int ROWS, int OVER, typename W>
+__device__ __forceinline__ void walk_share(const AttnArgs &A, const Share &r, Ring &ring, W wait)
 {
     const Batch &B = A.b;
     const int lane = threadIdx.x & 31;
     int b = 0, h = 0, i = 0, t = 0, n = 0;
     Seq s = {};
     if (r.count > 0) {   // the block and tile of the first unit: each lane looks through a part of the blocks
-        b = sh.start_b;
+        b = r.b;
         s = load_seq(B, b);
         n = blocks_of<ROWS>(B, s);
-        h = (int)(sh.start_off / sh.head_units);
-        const int64_t off = sh.start_off - h * sh.head_units;
+        h = (int)(r.off / r.head_units);
+        const int64_t off = r.off - h * r.head_units;
         const int each = (n + 31) / 32, i0 = min(n, lane * each), i1 = min(n, i0 + each);
         int64_t u = 0;
 #pragma unroll 1
