@@ -333,7 +333,9 @@ def _dtype(t) -> int:
 def _stream(stream) -> int | None:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without building a Stream object (3 us on the Arm host)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -527,59 +529,94 @@ def verify_commit_kn(state, conv_state, state_snap, conv_snap, n_accept, dims: D
 
 
 # ------------------------------------------------------------------ attention over the paged cache
-def _rows(t, name: str, dtypes, n_tokens: int, heads: int, dense: bool = False) -> tuple:
+# A single-token call takes a few microseconds on the GPU, so the checks below look at each tensor once, through
+# the attributes that cost least.
+_torch = None
+_BF16_DT = _ACT_DT = _I32_DT = ()
+
+
+def _load_torch():
+    global _torch, _BF16_DT, _ACT_DT, _I32_DT
+    if _torch is None:
+        import torch
+        _BF16_DT, _ACT_DT, _I32_DT = (torch.bfloat16,), (torch.float32, torch.bfloat16), (torch.int32,)
+        _torch = torch
+    return _torch
+
+
+def _refuse(t, name: str, dtypes, dev: int):
+    """Why a tensor argument is not one of dtypes on CUDA device dev, as an exception."""
+    if not isinstance(t, _torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d)[6:] for d in dtypes)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: tensor is on {t.device}, not on a CUDA device")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: tensor is on {t.device}, the current device is cuda:{dev}")
+
+
+def _rows(t, name: str, dtypes, n_tokens: int, heads: int, dev: int, dense: bool = False) -> tuple:
     """(address, row stride in elements) of a [n_tokens][heads][128] or [n_tokens][heads * 128] tensor
     whose rows may be farther apart than they are long. An int is a raw device address of dense rows."""
-    if t is None or isinstance(t, int):
-        return t, heads * 128
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
-    if t.dtype not in _torch_dtypes(*dtypes):
-        raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(dtypes)}")
+    width = heads * 128
+    if t is None or t.__class__ is int:
+        return t, width
+    if not isinstance(t, _torch.Tensor) or t.dtype not in dtypes:
+        _refuse(t, name, dtypes, dev)
     shape, stride = t.shape, t.stride()
-    if tuple(shape) not in ((n_tokens, heads, 128), (n_tokens, heads * 128)):
+    if shape != (n_tokens, heads, 128) and shape != (n_tokens, width):
         raise ValueError(f"{name}: shape {tuple(shape)}, expected ({n_tokens}, {heads}, 128)")
     if stride[-1] != 1 or (len(shape) == 3 and heads > 1 and stride[1] != 128):
         raise ValueError(f"{name}: elements of a row must be contiguous")
-    row = stride[0] if n_tokens > 1 else heads * 128
-    if dense and row != heads * 128:
+    row = stride[0] if n_tokens > 1 else width
+    if dense and row != width:
         raise ValueError(f"{name}: rows must be dense")
-    _on_device(t, name)
+    if t.get_device() != dev:
+        _refuse(t, name, dtypes, dev)
     return t.data_ptr(), row
 
 
-def _on_device(t, name: str):
-    import torch
-    if not t.is_cuda:
-        raise ValueError(f"{name}: tensor is on {t.device}, not on a CUDA device")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: tensor is on {t.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-
-
-def _counts(t, name: str, n: int) -> int | None:
-    if t is not None and not isinstance(t, int) and t.numel() != n:
+def _counts(t, name: str, n: int, dev: int) -> int | None:
+    """Address of a contiguous int32 tensor of n entries."""
+    if t is None or t.__class__ is int:
+        return t
+    if not isinstance(t, _torch.Tensor) or t.dtype not in _I32_DT:
+        _refuse(t, name, _I32_DT, dev)
+    if t.numel() != n:
         raise ValueError(f"{name}: {t.numel()} entries, expected {n}")
-    return _dev(t, name, _I32)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensor must be contiguous")
+    if t.get_device() != dev:
+        _refuse(t, name, _I32_DT, dev)
+    return t.data_ptr()
+
+
+def _device_and_stream(stream) -> tuple:
+    """(index of the current CUDA device, stream handle); the device is -2 where there is none, which no
+    tensor's checks pass."""
+    t = _torch or _load_torch()
+    if not t.cuda.is_available():
+        return -2, None
+    return t.cuda.current_device(), _stream(stream)
 
 
 def attn_append(q, k, v, cache: KvCache, q_start, kv_len, rope: Rope, q_out, dims: AttnDims, stream=None):
     """Rotate q into q_out, and rotate, quantise and append k and v; see gdn_attn_append. q and q_out
     may both be None."""
-    n = dims.n_tokens
-    kp, ks = _rows(k, "k", _ACT, n, dims.n_kv_heads)
-    vp, vs = _rows(v, "v", _ACT, n, dims.n_kv_heads)
-    qp, qs = _rows(q, "q", _ACT, n, dims.n_q_heads)
-    op, _ = _rows(q_out, "q_out", ("bfloat16",), n, dims.n_q_heads, dense=True)
-    for t, nm in ((v, "v"), (q, "q")):
-        if t is not None and t.dtype != k.dtype:
-            raise TypeError(f"{nm}: dtype {t.dtype}, k is {k.dtype}")
-    _check(load().gdn_attn_append(qp, qs, kp, ks, vp, vs, _dtype(k), cache._for(dims),
-                                  _counts(q_start, "q_start", dims.n_seq + 1),
-                                  _counts(kv_len, "kv_len", dims.n_seq), rope._ref, op, dims._ref,
-                                  _stream(stream)),
-           "gdn_attn_append")
+    dev, handle = _device_and_stream(stream)
+    n, hq, hkv = dims.n_tokens, dims.n_q_heads, dims.n_kv_heads
+    kp, ks = _rows(k, "k", _ACT_DT, n, hkv, dev)
+    same = (k.dtype,)
+    vp, vs = _rows(v, "v", same, n, hkv, dev)
+    qp, qs = _rows(q, "q", same, n, hq, dev)
+    op, _ = _rows(q_out, "q_out", _BF16_DT, n, hq, dev, True)
+    status = (_lib or load()).gdn_attn_append(
+        qp, qs, kp, ks, vp, vs, GDN_BF16 if same == _BF16_DT else GDN_F32, cache._for(dims),
+        _counts(q_start, "q_start", dims.n_seq + 1, dev), _counts(kv_len, "kv_len", dims.n_seq, dev), rope._ref, op,
+        dims._ref, handle)
+    if status:
+        _check(status, "gdn_attn_append")
 
 
 def attn_workspace_bytes(dims: AttnDims, prefill: bool = False) -> int:
@@ -587,18 +624,26 @@ def attn_workspace_bytes(dims: AttnDims, prefill: bool = False) -> int:
     return int(load().gdn_attn_workspace_bytes(dims._ref, int(prefill)))
 
 
-def _attend(fn: str, q, cache, q_start, kv_len, out, dims, scale, softcap, window, workspace, stream):
-    qp, qs = _rows(q, "q", ("bfloat16",), dims.n_tokens, dims.n_q_heads)
-    op, _ = _rows(out, "out", ("bfloat16",), dims.n_tokens, dims.n_q_heads, dense=True)
+def _attend(prefill: bool, q, cache, q_start, kv_len, out, dims, scale, softcap, window, workspace, stream):
+    dev, handle = _device_and_stream(stream)
+    n, hq = dims.n_tokens, dims.n_q_heads
+    qp, qs = _rows(q, "q", _BF16_DT, n, hq, dev)
+    op, _ = _rows(out, "out", _BF16_DT, n, hq, dev, True)
+    starts = _counts(q_start, "q_start", dims.n_seq + 1, dev)
+    lens = _counts(kv_len, "kv_len", dims.n_seq, dev)
+    lib = _lib or load()
     if workspace is None:
-        import torch
-        nbytes = attn_workspace_bytes(dims, fn == "gdn_attn_prefill")
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
-    _check(getattr(load(), fn)(qp, qs, cache._for(dims), _counts(q_start, "q_start", dims.n_seq + 1),
-                               _counts(kv_len, "kv_len", dims.n_seq), op, dims._ref,
-                               128 ** -0.5 if scale is None else scale, softcap, window, _ptr(workspace),
-                               workspace.numel() * workspace.element_size(), _stream(stream)),
-           fn)
+        nbytes = max(attn_workspace_bytes(dims, prefill), 16)
+        workspace = _torch.empty(nbytes, dtype=_torch.uint8, device=q.device)
+        if stream is not None:   # its memory is not handed out again before that stream is done with it
+            workspace.record_stream(_torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    elif not workspace.is_contiguous() or workspace.get_device() != dev:
+        _ptr(workspace)
+    status = (lib.gdn_attn_prefill if prefill else lib.gdn_attn_decode)(
+        qp, qs, cache._for(dims), starts, lens, op, dims._ref, 128 ** -0.5 if scale is None else scale, softcap,
+        window, workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle)
+    if status:
+        _check(status, "gdn_attn_prefill" if prefill else "gdn_attn_decode")
 
 
 def attn_decode(q, cache: KvCache, q_start, kv_len, out, dims: AttnDims, scale: float | None = None,
@@ -606,11 +651,11 @@ def attn_decode(q, cache: KvCache, q_start, kv_len, out, dims: AttnDims, scale: 
     """Attention of a few tokens per sequence over the cache; see gdn_attn_decode. scale: 1/sqrt(128)
     unless given. workspace: a device tensor of attn_workspace_bytes(dims) bytes; when None, one is
     allocated with torch for this call."""
-    _attend("gdn_attn_decode", q, cache, q_start, kv_len, out, dims, scale, softcap, window, workspace, stream)
+    _attend(False, q, cache, q_start, kv_len, out, dims, scale, softcap, window, workspace, stream)
 
 
 def attn_prefill(q, cache: KvCache, q_start, kv_len, out, dims: AttnDims, scale: float | None = None,
                  softcap: float = 0.0, window: int = 0, workspace=None, stream=None):
     """Attention of many tokens per sequence over the cache; see gdn_attn_prefill. workspace:
     attn_workspace_bytes(dims, prefill=True) bytes, or None."""
-    _attend("gdn_attn_prefill", q, cache, q_start, kv_len, out, dims, scale, softcap, window, workspace, stream)
+    _attend(True, q, cache, q_start, kv_len, out, dims, scale, softcap, window, workspace, stream)

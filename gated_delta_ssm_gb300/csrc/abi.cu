@@ -229,8 +229,9 @@ gdn_status check_attn_dims(const gdn_attn_dims *d)
     if (d->head_dim != gdn::kD || d->n_q_heads / d->n_kv_heads > gdn::attn::kMaxGroup ||
         (d->page_size != 16 && d->page_size != 32 && d->page_size != 64 && d->page_size != 128))
         return GDN_ERR_UNSUPPORTED;
-    // positions are 32-bit
-    return (int64_t)d->max_pages * d->page_size > (1 << 30) ? GDN_ERR_INVALID_ARG : GDN_OK;
+    if ((int64_t)d->max_pages * d->page_size > (1 << 30))   // positions are 32-bit
+        return GDN_ERR_INVALID_ARG;
+    return (int64_t)d->n_tokens * (d->n_q_heads / d->n_kv_heads) > gdn::attn::kMostRows ? GDN_ERR_UNSUPPORTED : GDN_OK;
 }
 
 // Checks of the cache and the batch description, and their copy for the kernels.
@@ -261,6 +262,7 @@ gdn_status attn_batch(const gdn_kv_cache *cache, const int32_t *q_start, const i
     b.max_pages = d->max_pages;
     b.n_tokens = d->n_tokens;
     b.max_q = d->max_q < d->n_tokens ? d->max_q : d->n_tokens;
+    b.inv_G = (uint32_t)((0x80000000u + b.G - 1) / b.G);
     return GDN_OK;
 }
 

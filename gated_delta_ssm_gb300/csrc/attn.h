@@ -12,6 +12,7 @@ constexpr int kErrMeta = 256;       // q_start, kv_len, page_table or a position
 constexpr int kErrNonFinite = 512;  // append: a key or value that is not finite
 constexpr int kErrWait = 1024;      // a bounded wait gave up
 
+constexpr int64_t kMostRows = (1 << 27) - 256;  // most (token, head of a group) rows of a call
 constexpr int kMaxGroup = 16;       // most q heads per KV head
 constexpr int kMaxDecodeRows = 64;  // most (head of a group, token) rows per KV head in a decode call
 
@@ -22,6 +23,7 @@ struct Batch {
     const int32_t *page_table;      // [n_seq][max_pages]
     const int32_t *q_start, *kv_len;
     int n_seq, Hq, Hkv, G, P, n_pages, max_pages, n_tokens, max_q;
+    uint32_t inv_G;                 // ceil(2^31 / G)
 };
 
 struct AppendArgs {

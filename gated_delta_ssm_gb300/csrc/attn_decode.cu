@@ -162,9 +162,17 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
     }
     if (warp == 1)
         tc::tmem_alloc(tc::smem_addr(&sh.tmem), C::kTmemCols);
-    // rows of P that no q row uses stay zero
-    for (uint32_t i = tid; i < 4 * C::kRowBytes / 16; i += kThreads)
-        reinterpret_cast<uint4 *>(mem + C::kP)[i] = make_uint4(0, 0, 0, 0);
+    // rows of Q and P that no q row uses stay zero
+    for (uint32_t i = tid; i < 8 * C::kRowBytes / 16; i += kThreads)
+        reinterpret_cast<uint4 *>(mem + C::kQ)[i] = make_uint4(0, 0, 0, 0);
+    if (tid < 2 * NR) {
+        sh.f[tid / NR][tid % NR] = 0.0f;
+        sh.limit[tid / NR][tid % NR] = -1;
+    }
+    if (tid == 32) {
+        asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&map_k)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&map_v)) : "memory");
+    }
     tc::fence_smem_to_async();
 
     wait_previous_grid();
@@ -322,7 +330,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
             if (k >= 2)
                 wait(sh.q_free[par], (k / 2 - 1) & 1);
 #pragma unroll 2
-            for (int r = r4; r < NR; r += 4) {
+            for (int r = r4; r < ((R + 3) & ~3); r += 4) {
                 const int tok = r * inv_G >> 16, g = r - tok * B.G;
                 const bool live = tok < w.n;
                 float v[16] = {};
@@ -649,6 +657,8 @@ cudaError_t launch_decode(const AttnArgs &args, cudaStream_t s)
     if (a.window == 0 || a.window > kNoWindow)
         a.window = kNoWindow;
     const int rows = b.G * b.max_q, most = most_ctas(rows, a.sm_count);
+    if (most_units(b, kMaxDecodeRows, kOver) > 2e9)
+        return cudaErrorInvalidConfiguration;
     const int64_t units = (((int64_t)b.max_pages * b.P + kTile - 1) / kTile + kOver) * b.n_seq * b.Hkv;
     const int grid = (int)(units < most ? units : most);
     switch (row_pad(rows)) {

@@ -17,6 +17,9 @@ struct Seq {
     bool ok;
 };
 
+// y / G for y below 2^27: with e = inv_G G - 2^31 < 16, 2 y e stays below 2^32.
+__device__ __forceinline__ int div_G(const Batch &B, int y) { return (int)__umulhi(2u * (uint32_t)y, B.inv_G); }
+
 // Reads and checks sequence b. An entry out of range gives ok = false and n = 0.
 __device__ __forceinline__ Seq load_seq(const Batch &B, int b)
 {

@@ -366,6 +366,10 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
     }
     if (warp == 1)
         tc::tmem_alloc(tc::smem_addr(&sh.tmem), kTmemCols);
+    if (tid == 96) {
+        asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&map_k)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&map_v)) : "memory");
+    }
     wait_previous_grid();
     Share share = {};
     if (B.n_seq > kFewSeqs)
@@ -834,6 +838,8 @@ cudaError_t launch_prefill(const AttnArgs &args, cudaStream_t s)
     const Batch &b = a.b;
     if (a.window == 0 || a.window > kNoWindow)
         a.window = kNoWindow;
+    if (most_units(b, kRows, kOver) > 2e9)
+        return cudaErrorInvalidConfiguration;
     const int64_t tiles = ((int64_t)b.max_pages * b.P + kTile - 1) / kTile;
     const int64_t blocks = ((int64_t)b.max_q * b.G + kRows - 1) / kRows * b.Hkv * b.n_seq;
     const int64_t units = tiles >= a.sm_count || blocks >= a.sm_count ? a.sm_count : (tiles + kOver) * blocks;

@@ -42,39 +42,48 @@ constexpr int kFewSeqs = 256;
 
 template <int THREADS>
 struct ShareShared {
-    int64_t warp_sum[THREADS / 32];
-    int64_t total;
-    int64_t start_off, head_units;    // the share's first unit within its sequence; units of one KV head there
+    int warp_sum[THREADS / 32];
+    int start_off, head_units;        // the share's first unit within its sequence; units of one KV head there
     int start_b;
+    Seq start_seq;
 };
 
+// Units are 32-bit numbers: most_units bounds them on the host. Of `total` units, the first `more` of n_cta
+// shares take each + 1, the others `each`: one short division for all that a walk needs.
 struct Share {
-    int64_t total, first;             // units of the batch; the share's first
-    int n_cta, count;                 // CTAs with a share; units of this one's
-    int b;                            // the first unit's sequence,
-    int64_t off, head_units;          // its place among that sequence's units, and those of one KV head
+    int n_cta, each, more;
+    int first, count;                 // this CTA's first unit, and its units
+    int b, off, head_units;           // the first unit's sequence, its place there, units of one KV head there
+    Seq s;
 };
 
-__device__ __forceinline__ int64_t share_begin(int64_t total, int n, int c) { return total * c / n; }
-__device__ __forceinline__ int share_of(int64_t total, int n, int64_t unit)
+__device__ __forceinline__ int share_of(const Share &r, int unit)
 {
-    return (int)(((unit + 1) * n - 1) / total);
+    const int bulk = r.more * (r.each + 1);
+    return unit < bulk ? unit / (r.each + 1) : r.more + (unit - bulk) / r.each;
+}
+
+// At least the units of any batch of these dimensions.
+inline double most_units(const Batch &b, int rows, int over)
+{
+    const double tiles = (double)(((int64_t)b.max_pages * b.P + kTile - 1) / kTile) + 1 + over;
+    return ((double)b.n_tokens * b.G / rows + b.n_seq) * b.Hkv * tiles;
 }
 
 // Blocks of a sequence; none where there are no keys.
 template <int ROWS>
 __device__ __forceinline__ int blocks_of(const Batch &B, const Seq &s)
 {
-    return s.L > 0 ? (int)(((int64_t)s.n * B.G + ROWS - 1) / ROWS) : 0;
+    return s.L > 0 ? (int)((unsigned)(s.n * B.G + ROWS - 1) / ROWS) : 0;
 }
 
 // Key positions [lo, hi] that block i of a sequence sees, at least [0, 0].
 template <int ROWS>
 __device__ __forceinline__ void block_keys(const AttnArgs &A, const Seq &s, int i, int &lo, int &hi)
 {
-    const int G = A.b.G, first = s.L - s.n;
-    lo = max(0, first + i * ROWS / G - A.window + 1);
-    hi = max(0, first + min((i * ROWS + ROWS - 1) / G, s.n - 1));
+    const int first = s.L - s.n;
+    lo = max(0, first + div_G(A.b, i * ROWS) - A.window + 1);
+    hi = max(0, first + min(div_G(A.b, i * ROWS + ROWS - 1), s.n - 1));
 }
 
 template <int ROWS, int OVER>
@@ -87,11 +96,11 @@ __device__ __forceinline__ int block_units(const AttnArgs &A, const Seq &s, int 
 
 // Units of one KV head of a sequence: blocks from, from + step, ..
 template <int ROWS, int OVER>
-__device__ __forceinline__ int64_t head_units(const AttnArgs &A, int b, int from, int step)
+__device__ __forceinline__ int head_units(const AttnArgs &A, int b, int from, int step)
 {
     const Seq s = load_seq(A.b, b);
     const int n = blocks_of<ROWS>(A.b, s);
-    int64_t u = 0;
+    int u = 0;
 #pragma unroll 1
     for (int i = from; i < n; i += step)
         u += block_units<ROWS, OVER>(A, s, i);
@@ -111,48 +120,51 @@ __device__ __forceinline__ Share find_share(const AttnArgs &A, ShareShared<THREA
         g *= 2;
     const int per = g > 1 ? 1 : (B.n_seq + threads - 1) / threads;
     const int first_b = (tid / g) * per, sub = tid % g;
-    int64_t mine = 0;
+    int mine = 0;
 #pragma unroll 2
     for (int i = 0; i < per; ++i)
         if (first_b + i < B.n_seq)
             mine += head_units<ROWS, OVER>(A, first_b + i, sub, g);
     for (int m = 1; m < g; m <<= 1)
         mine += __shfl_xor_sync(0xffffffffu, mine, m);
-    const int64_t one_head = mine;
+    const int one_head = mine;
     mine = sub == 0 ? mine * B.Hkv : 0;
-    int64_t incl = mine;
+    int incl = mine;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, incl, m);
+        const int up = __shfl_up_sync(0xffffffffu, incl, m);
         if (lane >= m)
             incl += up;
     }
     Share r;
-    r.total = __shfl_sync(0xffffffffu, incl, 31);
+    int total = __shfl_sync(0xffffffffu, incl, 31);
     if (threads > 32) {
         if (lane == 31)
             sh.warp_sum[warp] = incl;
         sync();
-        r.total = 0;
+        total = 0;
 #pragma unroll 1
         for (int i = 0; i < threads / 32; ++i) {
             incl += i < warp ? sh.warp_sum[i] : 0;
-            r.total += sh.warp_sum[i];
+            total += sh.warp_sum[i];
         }
     }
-    r.n_cta = (int)min((int64_t)gridDim.x, r.total);
-    const bool works = (int)blockIdx.x < r.n_cta;
-    r.first = works ? share_begin(r.total, r.n_cta, blockIdx.x) : 0;
-    r.count = works ? (int)(share_begin(r.total, r.n_cta, blockIdx.x + 1) - r.first) : 0;
-    if (works && r.first < incl && r.first >= incl - mine) {   // among this thread's sequences
-        int64_t at = incl - mine;
+    const int c = blockIdx.x;
+    r.n_cta = min((int)gridDim.x, total);
+    r.each = r.n_cta > 0 ? total / r.n_cta : 1;
+    r.more = total - r.each * r.n_cta;
+    r.first = r.each * c + min(c, r.more);
+    r.count = c < r.n_cta ? r.each + (c < r.more ? 1 : 0) : 0;
+    if (r.count > 0 && r.first < incl && r.first >= incl - mine) {   // among this thread's sequences
+        int at = incl - mine;
 #pragma unroll 1
         for (int i = 0; i < per && first_b + i < B.n_seq; ++i) {
-            const int64_t u = g > 1 ? one_head : head_units<ROWS, OVER>(A, first_b + i, 0, 1);
+            const int u = g > 1 ? one_head : head_units<ROWS, OVER>(A, first_b + i, 0, 1);
             if (r.first < at + u * B.Hkv) {
                 sh.start_b = first_b + i;
                 sh.start_off = r.first - at;
                 sh.head_units = u;
+                sh.start_seq = load_seq(B, first_b + i);
                 break;
             }
             at += u * B.Hkv;
@@ -162,6 +174,7 @@ __device__ __forceinline__ Share find_share(const AttnArgs &A, ShareShared<THREA
     r.b = sh.start_b;
     r.off = sh.start_off;
     r.head_units = sh.head_units;
+    r.s = sh.start_seq;
     return r;
 }
 
@@ -175,24 +188,27 @@ __device__ __forceinline__ void walk_share(const AttnArgs &A, const Share &r, Ri
     Seq s = {};
     if (r.count > 0) {   // the block and tile of the first unit: each lane looks through a part of the blocks
         b = r.b;
-        s = load_seq(B, b);
+        s = r.s;
         n = blocks_of<ROWS>(B, s);
-        h = (int)(r.off / r.head_units);
-        const int64_t off = r.off - h * r.head_units;
+        h = r.off < r.head_units ? 0 : r.off / r.head_units;
+        t = r.off - h * r.head_units;
+    }
+    if (n > 1) {
+        const int off = t;
         const int each = (n + 31) / 32, i0 = min(n, lane * each), i1 = min(n, i0 + each);
-        int64_t u = 0;
+        int u = 0;
 #pragma unroll 1
         for (int k = i0; k < i1; ++k)
             u += block_units<ROWS, OVER>(A, s, k);
-        int64_t upto = u;
+        int upto = u;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
-            const int64_t up = __shfl_up_sync(0xffffffffu, upto, m);
+            const int up = __shfl_up_sync(0xffffffffu, upto, m);
             if (lane >= m)
                 upto += up;
         }
         const bool here = off < upto && off >= upto - u;
-        int64_t at = upto - u;
+        int at = upto - u;
         if (here)
 #pragma unroll 1
             for (i = i0; i < i1; ++i) {
@@ -203,10 +219,10 @@ __device__ __forceinline__ void walk_share(const AttnArgs &A, const Share &r, Ri
             }
         const int from = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
         i = __shfl_sync(0xffffffffu, i, from & 31);
-        t = __shfl_sync(0xffffffffu, (int)(off - at), from & 31);
+        t = __shfl_sync(0xffffffffu, off - at, from & 31);
     }
     int left = r.count;
-    int64_t unit = r.first;
+    int unit = r.first;
 #pragma unroll 1
     for (int k = 0;;) {
         Seg q = {};
@@ -219,11 +235,11 @@ __device__ __forceinline__ void walk_share(const AttnArgs &A, const Share &r, Ri
             q.kt = lo / kTile + t0;
             q.b = b, q.h = h, q.row0 = s.row0, q.n = s.n, q.first = s.L - s.n, q.lo = lo, q.hi = hi;
             q.blk = i * ROWS;
-            q.tok0 = q.blk / B.G;
+            q.tok0 = div_G(B, q.blk);
             q.rem0 = q.blk - q.tok0 * B.G;
             q.begins = t0 == 0;
             q.whole = q.nt == all;
-            q.last_cta = share_of(r.total, r.n_cta, unit + (all + OVER - t) - 1);
+            q.last_cta = share_of(r, unit + (all + OVER - t) - 1);
             left -= end - t;
             unit += end - t;
             t = 0;

@@ -54,6 +54,7 @@ BAD_DIMS = [
     (dict(n_kv_heads=0), BAD), (dict(n_pages=0), BAD), (dict(max_pages=0), BAD), (dict(n_tokens=0), BAD),
     (dict(max_q=0), BAD), (dict(head_dim=0), BAD), (dict(page_size=0), BAD),
     (dict(max_pages=1 << 25), BAD),                                  # positions past 2^30
+    (dict(n_tokens=1 << 26), UNSUPPORTED),                           # 2^28 (token, head of a group) rows
     (dict(head_dim=64), UNSUPPORTED), (dict(page_size=48), UNSUPPORTED), (dict(page_size=256), UNSUPPORTED),
     (dict(n_q_heads=34, n_kv_heads=2), UNSUPPORTED),                 # 17 q heads per KV head
 ]
