@@ -25,8 +25,9 @@
 //
 // Roles of a CTA: warp 0 copies pages to shared memory, warp 1 issues the
 // products, warp 2 splits the q rows of the next segment, warp 3 walks the share,
-// warps 4-7 hold a key per thread and turn scores into weights, warps 8-11 hold a
-// dimension per thread and join the products.
+// one or two groups of four warps hold a key per thread and turn scores into
+// weights, and the last four warps hold a dimension per thread and join the
+// products.
 #include "attn_share.cuh"
 #include "attn_tc.cuh"
 #include "cluster.cuh"
@@ -39,7 +40,6 @@ static __device__ int g_attn_decode_error;
 
 namespace {
 
-constexpr int kThreads = 384;
 constexpr int kOver = 1;     // what a block costs besides its tiles, in tiles
 constexpr float kNoRef = -1e30f;   // below every reference, and finite: 2^(-inf - kNoRef) is 0
 
@@ -57,6 +57,9 @@ struct Cfg {
     static constexpr int kO = NR == 64 ? 1 : 2;
     static constexpr uint32_t kTmemCols = NR == 16 ? 256 : 512;
     static constexpr int kLs = (NR + 31) / 32;
+    // groups of four warps that turn scores into weights, eight rows in turn each
+    static constexpr int kWgs = NR == 16 ? 1 : 2;
+    static constexpr int kThreads = 256 + 128 * kWgs;
 };
 
 template <int NR>
@@ -65,21 +68,25 @@ struct Shared {
     uint64_t s_full[2], p_full[2], o_full[2], o_free[2], q_full[2], q_free[2], l_full[2], l_free[2], coef_full[4];
     uint32_t tmem;
     volatile int abort;
-    ShareShared<kThreads> share;
+    ShareShared<Cfg<NR>::kThreads> share;
     Ring ring;
-    float4 top[4][NR];         // of four tiles: the warps' maxima of each row
+    float4 top[4][NR];         // of four tiles: the warps' maxima of each row,
+    float4 scale[2][NR];       // and, of two, 2^(maximum - o_ref)
     float f[2][NR];            // scale * log2 e / (power of two of the q row)
     int limit[2][NR];          // position of each row
     float l_sum[2][4][NR], l_ref[2][4][NR];
     float o_ref[NR];
 };
 
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8])
+// 8 columns of this thread's lane, without waiting, and the wait for them.
+__device__ __forceinline__ void tmem_get8(uint32_t taddr, uint32_t (&r)[8])
 {
-    uint32_t r[8];
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait8(uint32_t (&r)[8], float (&v)[8])
+{
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
                  :: "memory");
@@ -88,13 +95,16 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8])
         v[i] = __uint_as_float(r[i]);
 }
 
-// 4 columns of each of the four warps' products, `step` columns apart.
-__device__ __forceinline__ void tmem_ld4x4(uint32_t taddr, uint32_t step, uint32_t (&r)[4][4])
+// 4 columns of each of the four warps' products, `step` columns apart, without waiting, and the wait.
+__device__ __forceinline__ void tmem_get4x4(uint32_t taddr, uint32_t step, uint32_t (&r)[4][4])
 {
 #pragma unroll
     for (int w = 0; w < 4; ++w)
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(r[w][0]), "=r"(r[w][1]), "=r"(r[w][2]), "=r"(r[w][3]) : "r"(taddr + w * step));
+}
+__device__ __forceinline__ void tmem_wait4x4(uint32_t (&r)[4][4])
+{
 #pragma unroll
     for (int w = 0; w < 4; ++w)
         asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -125,11 +135,12 @@ __device__ __forceinline__ float sum8(const float (&v)[8], int lane)
 }
 
 template <int NR>
-__global__ void __launch_bounds__(kThreads, Cfg<NR>::kCtas)
+__global__ void __launch_bounds__(Cfg<NR>::kThreads, Cfg<NR>::kCtas)
 attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v)
 {
     using C = Cfg<NR>;
+    constexpr int kThreads = C::kThreads;
     extern __shared__ __align__(1024) uint8_t dyn[];
     __shared__ Shared<NR> sh;
     const Batch &B = A.b;
@@ -144,16 +155,16 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
             init(sh.full[i], 1), init(sh.empty[i], 1);
         for (int i = 0; i < 2; ++i) {
             init(sh.s_full[i], 1);
-            init(sh.p_full[i], 128);
+            init(sh.p_full[i], 128 * C::kWgs);
             init(sh.o_full[i], 1);
             init(sh.o_free[i], 128);
             init(sh.q_full[i], 32);
-            init(sh.q_free[i], 129);
-            init(sh.l_full[i], 128);
+            init(sh.q_free[i], 128 * C::kWgs + 1);
+            init(sh.l_full[i], 128 * C::kWgs);
             init(sh.l_free[i], 128);
         }
         for (int i = 0; i < 4; ++i)
-            init(sh.coef_full[i], 4);
+            init(sh.coef_full[i], 4 * C::kWgs);
         for (int i = 0; i < kRing; ++i)
             init(sh.ring.full[i], 1), init(sh.ring.free[i], kThreads / 32 - 1);   // every warp but the walker
         init(sh.drain, 1);
@@ -181,7 +192,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
         share = find_share<kMaxDecodeRows, kOver>(A, sh.share, tid, kThreads, [] { __syncthreads(); });
     PartMeta *const meta = reinterpret_cast<PartMeta *>(A.ws);
     float *const parts = part_slots(A.ws, gridDim.x);
-    if (tid == 256)   // the thread that may describe a block later
+    if (tid == kThreads - 128)   // the thread that may describe a block later
         meta[blockIdx.x].owner = 0;
     tc::fence_before_sync();
     __syncthreads();
@@ -361,11 +372,13 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
             share = find_share<kMaxDecodeRows, kOver>(A, sh.share, lane, 32, [] { __syncwarp(); });
         walk_share<kMaxDecodeRows, kOver>(A, share, sh.ring, wait);
         clear_empty(A, &g_attn_decode_error);
-    } else if (warp < 8) {
+    } else if (warp < 4 + 4 * C::kWgs) {
         // ------------------------------------------------------------ scores to weights: a key per thread
-        const int t128 = tid - 128, wq = warp & 3;
+        const int t128 = tid & 127, wq = warp & 3, wg = (warp >> 2) - 1;
+        const int row8 = lane & 7;
         const uint32_t s_at = tmem + ((uint32_t)(wq * 32) << 16);
-        const float cap2 = A.softcap * kLog2e, inv_cap2 = A.softcap > 0.0f ? 1.0f / cap2 : 0.0f;
+        const float cap2 = A.softcap * kLog2e, cap_in = 2.0f * kLog2e / cap2;
+        const int cap = cap_mode(A.softcap);
         int i = 0;
 #pragma unroll 1
         for (int k = 0;; ++k) {
@@ -409,21 +422,38 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
                 uint8_t *const prow = mem + C::kP + par * 2 * C::kRowBytes + (t128 & 15);
                 wait(sh.s_full[par], (i >> 1) & 1);
                 tc::fence_after_sync();
+                uint32_t next[8];
+                tmem_get8(s_at + par * NR + 8 * wg, next);
 #pragma unroll 1
-                for (int c = 0; c < chunks; ++c) {
+                for (int c = wg; c < chunks; c += C::kWgs) {
                     float x[8];
-                    tmem_ld8(s_at + par * NR + 8 * c, x);
+                    tmem_wait8(next, x);
+                    if (c + C::kWgs < chunks)
+                        tmem_get8(s_at + par * NR + 8 * (c + C::kWgs), next);
                     const float4 f0 = *reinterpret_cast<const float4 *>(&sh.f[par_q][8 * c]);
                     const float4 f1 = *reinterpret_cast<const float4 *>(&sh.f[par_q][8 * c + 4]);
-                    const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
-                    if (A.softcap > 0.0f) {
+                    const uint64_t f2[4] = {pack2(f0.x, f0.y), pack2(f0.z, f0.w), pack2(f1.x, f1.y), pack2(f1.z, f1.w)};
+                    const uint64_t ks2 = pack2(ks, ks), ev2 = pack2(ev, ev);
+                    if (cap == kNoCap) {
 #pragma unroll
-                        for (int r = 0; r < 8; ++r)
-                            x[r] = fmaf(cap2, tanh_cap(x[r] * (f[r] * ks) * inv_cap2), ev);
+                        for (int r = 0; r < 8; r += 2) {
+                            const float2 y = unpack2(fma2(pack2(x[r], x[r + 1]), mul2(f2[r / 2], ks2), ev2));
+                            x[r] = y.x, x[r + 1] = y.y;
+                        }
+                    } else if (cap == kLowCap) {   // c - 2 c / (1 + e^(2 s / cap)); tanh is 1 past an exponent of 60
+#pragma unroll
+                        for (int r = 0; r < 8; r += 2) {
+                            const float2 y = unpack2(mul2(pack2(x[r], x[r + 1]), mul2(f2[r / 2], ks2)));
+                            const float a = 1.0f + ex2(fminf(y.x * cap_in, 60.0f));
+                            const float b = 1.0f + ex2(fminf(y.y * cap_in, 60.0f));
+                            x[r] = fmaf(rcp(a), -2.0f * cap2, cap2 + ev);
+                            x[r + 1] = fmaf(rcp(b), -2.0f * cap2, cap2 + ev);
+                        }
                     } else {
+                        const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
                         for (int r = 0; r < 8; ++r)
-                            x[r] = fmaf(x[r], f[r] * ks, ev);
+                            x[r] = fmaf(cap2, tanh_cap(x[r] * (f[r] * ks) / cap2), ev);
                     }
                     if (!whole) {
 #pragma unroll
@@ -437,12 +467,13 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
 #pragma unroll
                     for (int r = 0; r < 8; r += 2) {
                         const float m0 = redux_max(x[r]), m1 = redux_max(x[r + 1]);
-                        mine = (lane & 7) == r ? m0 : (lane & 7) == r + 1 ? m1 : mine;
-                        // P is 2^(w - max + 8): at most 256
-                        const float z0 = ex2(x[r] - (m0 == -INFINITY ? 0.0f : m0 - 8.0f));
-                        const float z1 = ex2(x[r + 1] - (m1 == -INFINITY ? 0.0f : m1 - 8.0f));
-                        sums[r] = z0 * iv;
-                        sums[r + 1] = z1 * iv;
+                        mine = row8 == r ? m0 : row8 == r + 1 ? m1 : mine;
+                        // P is 2^(w - max + 8): at most 256; a row without visible keys has no maximum
+                        const float2 y = unpack2(add2(pack2(x[r], x[r + 1]), pack2(8.0f - fmaxf(m0, kNoRef),
+                                                                                   8.0f - fmaxf(m1, kNoRef))));
+                        const float z0 = ex2(y.x), z1 = ex2(y.y);
+                        const float2 q = unpack2(mul2(pack2(z0, z1), pack2(iv, iv)));
+                        sums[r] = q.x, sums[r + 1] = q.y;
                         uint32_t h8, l8;
                         split_e4m3(z0, z1, h8, l8);
                         uint8_t *a = p8 + r * 128 + (((t128 >> 4) ^ r) << 4);
@@ -454,7 +485,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
                     }
                     const float sum = sum8(sums, lane);
                     if ((lane >> 3) == (c & 3)) {     // the lane that keeps row 8 c + (lane & 7)
-                        reinterpret_cast<float *>(&sh.top[i & 3][8 * c + (lane & 7)])[wq] = mine;
+                        reinterpret_cast<float *>(&sh.top[i & 3][8 * c + row8])[wq] = mine;
 #pragma unroll
                         for (int e = 0; e < C::kLs; ++e) {
                             if (e != c >> 2)
@@ -472,7 +503,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
                 __syncwarp();
                 if (lane == 0)
                     arrive(sh.coef_full[i & 3]);
-                if (dead) {
+                if (dead && wg == 0) {
                     // nothing of the cache lies here, or nothing that may be seen: any code, NaN among
                     // them; its value row is cleared so that weight 0 gives 0
                     const int item = 2 * i + 1, st = item % C::kItems;
@@ -492,7 +523,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
                 wait(sh.l_free[par_q], (k / 2 - 1) & 1);
 #pragma unroll
             for (int e = 0; e < C::kLs; ++e)
-                if (32 * e + lane < NR) {
+                if (32 * e + lane < NR && ((lane >> 3) & (C::kWgs - 1)) == wg) {
                     sh.l_sum[par_q][wq][32 * e + lane] = l[e];
                     sh.l_ref[par_q][wq][32 * e + lane] = big[e];
                 }
@@ -500,7 +531,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
         }
     } else {
         // ------------------------------------------------------------ products joined: a dimension per thread
-        const int d = tid - 256, wq = warp & 3;
+        const int d = tid & 127, wq = warp & 3;
         const uint32_t o_at = tmem + 2 * NR + ((uint32_t)(wq * 32) << 16);
         int i = 0;
 #pragma unroll 1
@@ -521,17 +552,18 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
             for (int t = 0; t < w.nt; ++t, ++i) {
                 const int ob = i % C::kO;
                 wait(sh.coef_full[i & 3], (i >> 2) & 1);
-                // the references lag: sums of 32 bits do not mind 2^60
+                // a (row, warp) pair per thread: its scale. The references lag: sums of 32 bits do not mind 2^60
                 bool move = false;
-                if (lane < R) {
 #pragma unroll
-                    for (int e = 0; e < C::kLs; ++e) {
-                        const float4 m = sh.top[i & 3][32 * e + lane < R ? 32 * e + lane : lane];
-                        move |= fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)) >
-                                sh.o_ref[32 * e + lane < R ? 32 * e + lane : lane] + 60.0f;
+                for (int e = 0; e < (4 * NR + 127) / 128; ++e) {
+                    const int r = 32 * e + (d >> 2);
+                    if (r < R) {
+                        const float m = reinterpret_cast<const float *>(&sh.top[i & 3][r])[d & 3] - sh.o_ref[r];
+                        move |= m > 60.0f;
+                        reinterpret_cast<float *>(&sh.scale[i & 1][r])[d & 3] = ex2(m);
                     }
                 }
-                if (__any_sync(0xffffffffu, move)) {   // the same in all four warps
+                if (named_any(1, 128, move)) {
 #pragma unroll
                     for (int r = 0; r < NR; ++r) {
                         if (r % 4 == 0 && r >= R)
@@ -543,28 +575,32 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
                     named_sync(1, 128);
                     if (d < R) {
                         const float4 m = sh.top[i & 3][d];
-                        sh.o_ref[d] = fmaxf(sh.o_ref[d], fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)));
+                        const float ref = fmaxf(sh.o_ref[d], fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)));
+                        sh.o_ref[d] = ref;
+                        sh.scale[i & 1][d] = make_float4(ex2(m.x - ref), ex2(m.y - ref), ex2(m.z - ref), ex2(m.w - ref));
                     }
                     named_sync(1, 128);
                 }
                 wait(sh.o_full[ob], (i / C::kO) & 1);
                 tc::fence_after_sync();
+                uint32_t next[2][4][4];
+                tmem_get4x4(o_at + 4 * ob * NR, NR, next[0]);
 #pragma unroll
                 for (int c = 0; c < NR / 4; ++c) {
                     if (4 * c >= R)
                         break;
-                    uint32_t x[4][4];
-                    tmem_ld4x4(o_at + 4 * ob * NR + 4 * c, NR, x);
-                    const float4 refs = *reinterpret_cast<const float4 *>(&sh.o_ref[4 * c]);
-                    const float ref[4] = {refs.x, refs.y, refs.z, refs.w};
+                    uint32_t(&x)[4][4] = next[c & 1];
+                    tmem_wait4x4(x);
+                    if (c + 1 < NR / 4 && 4 * c + 4 < R)
+                        tmem_get4x4(o_at + 4 * ob * NR + 4 * c + 4, NR, next[(c + 1) & 1]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int r = 4 * c + e;
-                        const float4 m = sh.top[i & 3][r];
-                        o[r] = fmaf(__uint_as_float(x[0][e]), ex2(m.x - ref[e]), o[r]);
-                        o[r] = fmaf(__uint_as_float(x[1][e]), ex2(m.y - ref[e]), o[r]);
-                        o[r] = fmaf(__uint_as_float(x[2][e]), ex2(m.z - ref[e]), o[r]);
-                        o[r] = fmaf(__uint_as_float(x[3][e]), ex2(m.w - ref[e]), o[r]);
+                        const float4 m = sh.scale[i & 1][r];
+                        o[r] = fmaf(__uint_as_float(x[0][e]), m.x, o[r]);
+                        o[r] = fmaf(__uint_as_float(x[1][e]), m.y, o[r]);
+                        o[r] = fmaf(__uint_as_float(x[2][e]), m.z, o[r]);
+                        o[r] = fmaf(__uint_as_float(x[3][e]), m.w, o[r]);
                     }
                 }
                 tc::fence_before_sync();
@@ -633,7 +669,7 @@ cudaError_t launch_rows(const AttnArgs &a, int grid, cudaStream_t s)
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(Cfg<NR>::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;

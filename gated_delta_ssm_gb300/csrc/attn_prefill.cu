@@ -48,11 +48,6 @@ constexpr uint32_t kTmemCols = 512;           // S of A, S of B, O of A, O of B:
 // numbers of 8 exponent bits, so a reference that lags behind costs no precision, only range.
 constexpr float kSlack = 8.0f, kSlackSum = 65536.0f;   // 128 weights of at most 2^8 sum to 2^15
 
-// How scores are capped: not, so low that weights need no reference, or anyhow.
-enum { kNoCap = 0, kLowCap = 1, kAnyCap = 2 };
-// In base 2: sums of 2^30 weights stay below 2^110; and the factor 2 log2 e / cap stays finite.
-constexpr float kMostCap = 80.0f, kLeastCap = 1e-6f;
-
 struct Shared {
     uint64_t k_full[kKs], k_free[kKs], v_full[kVs], v_free[kVs], b_full[kVb], b_free[kVb];
     uint64_t q_full[2], s_full[2], p_full[2], o_done[2], drain[2];
@@ -117,44 +112,6 @@ __device__ __forceinline__ float score(float s, float fk, float cap2, float inv_
         return cap2 * tanh_cap(s * fk * inv_cap2);
     else
         return s * fk;
-}
-
-// a * b + c and a + b of two packed floats.
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ float rcp(float x)
-{
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint64_t pack2(float lo, float hi)
-{
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-    return d;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t a)
-{
-    float2 d;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(a));
-    return d;
 }
 
 // 16 columns of this thread's lane, without waiting, and the wait for them.
@@ -844,9 +801,11 @@ cudaError_t launch_prefill(const AttnArgs &args, cudaStream_t s)
     const int64_t blocks = ((int64_t)b.max_q * b.G + kRows - 1) / kRows * b.Hkv * b.n_seq;
     const int64_t units = tiles >= a.sm_count || blocks >= a.sm_count ? a.sm_count : (tiles + kOver) * blocks;
     const int grid = (int)(units < a.sm_count ? units : a.sm_count);
-    if (a.softcap == 0.0f)
-        return launch_cap<kNoCap>(a, grid, s);
-    return a.softcap * kLog2e <= kMostCap && a.softcap >= kLeastCap ? launch_cap<kLowCap>(a, grid, s) : launch_cap<kAnyCap>(a, grid, s);
+    switch (cap_mode(a.softcap)) {
+    case kNoCap: return launch_cap<kNoCap>(a, grid, s);
+    case kLowCap: return launch_cap<kLowCap>(a, grid, s);
+    default: return launch_cap<kAnyCap>(a, grid, s);
+    }
 }
 
 cudaError_t take_prefill_error(int *code)

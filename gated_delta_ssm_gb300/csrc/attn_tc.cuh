@@ -44,6 +44,53 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// How scores are capped: not, so low that weights need no reference, or anyhow.
+enum { kNoCap = 0, kLowCap = 1, kAnyCap = 2 };
+// In base 2: sums of 2^30 weights stay below 2^110; and the factor 2 log2 e / cap stays finite.
+constexpr float kMostCap = 80.0f, kLeastCap = 1e-6f;
+__host__ __device__ inline int cap_mode(float softcap)
+{
+    return softcap == 0.0f ? kNoCap : softcap * kLog2e <= kMostCap && softcap >= kLeastCap ? kLowCap : kAnyCap;
+}
+
+// a * b + c and a + b of two packed floats.
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint64_t pack2(float lo, float hi)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t a)
+{
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(a));
+    return d;
+}
+
 __device__ __forceinline__ void named_sync(int id, int threads)
 {
     asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
@@ -140,6 +187,16 @@ __device__ __forceinline__ bool wait_phase(uint32_t mbar, uint32_t parity, uint6
                 return false;
         }
     }
+}
+
+// Whether any of the threads that meet at a named barrier says so.
+__device__ __forceinline__ bool named_any(int id, int threads, bool mine)
+{
+    uint32_t any;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %3, 0;\n\tbarrier.cta.red.or.pred q, %1, %2, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(any) : "r"(id), "r"(threads), "r"((uint32_t)mine) : "memory");
+    return any != 0;
 }
 
 // One box (one page of one head: P rows of 128 bytes) into shared memory.
