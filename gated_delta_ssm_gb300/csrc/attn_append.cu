@@ -3,11 +3,12 @@
 // write them into the paged cache.
 //
 // Bound by memory: every input element is read once, q written as bf16 and k, v
-// as one byte. Work is cut so that no block waits for another:
-//   cache blocks  one CTA per (sequence, page the call touches, KV head, K or V).
-//                 It sees all of the page's new tokens at once, so the page's
-//                 scale is a block reduction over values that stay in registers.
-//   q blocks      kQRows (token, head) rows of one sequence per CTA.
+// as one byte. Work is cut so that no group of threads waits for another:
+//   cache groups  a CTA (or a warp, where a call brings a sequence at most four
+//                 tokens) per page the call touches, KV head, K or V. It sees all
+//                 of the page's new tokens at once, so the page's scale is a
+//                 reduction over values that stay in registers.
+//   q groups      eight threads per (token, few heads).
 // Eight threads share a row of 128, each with two 8-element pieces that hold the
 // two members of 8 rotation pairs, so a pair never leaves its thread:
 //   halves        pieces u*8 and rot/2 + u*8 while u < rot/16, then the 16
@@ -17,6 +18,7 @@
 #include <cuda_fp8.h>
 
 #include "attn_device.cuh"
+#include "cluster.cuh"
 #include "gdn_device.cuh"
 
 namespace gdn {
@@ -25,28 +27,47 @@ namespace attn {
 static __device__ int g_append_error;
 
 constexpr float kMinScale = 7.888609052210118e-31f;   // 2^-100
-constexpr int kQRows = 64;                            // (token, head) rows per q block
 
 struct Row16 {
     float a[8], b[8];
 };
 
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8])
-{
-    const uint4 r = __ldg(reinterpret_cast<const uint4 *>(p));
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+// Eight elements as they lie in memory.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 r;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { r = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void get(float (&v)[8]) const
+    {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
     }
-}
+};
+template <>
+struct Raw8<float> {
+    float4 x, y;
+    __device__ __forceinline__ void load(const float *p)
+    {
+        x = __ldg(reinterpret_cast<const float4 *>(p));
+        y = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const
+    {
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+        v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+    }
+};
 __device__ __forceinline__ void load8(const float *p, float (&v)[8])
 {
-    const float4 x = __ldg(reinterpret_cast<const float4 *>(p));
-    const float4 y = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-    v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+    Raw8<float> r;
+    r.load(p);
+    r.get(v);
 }
 
 // First elements of thread u's two pieces.
@@ -75,24 +96,34 @@ __device__ __forceinline__ void rotate_pair(float &a, float &b, float c, float s
     a = x;
 }
 
-__device__ __forceinline__ void rotate_row(Row16 &r, const AppendArgs &A, int u, int pos)
+struct Angles {
+    float c[8], s[8];
+};
+
+// Thread u's eight angles of a position.
+__device__ __forceinline__ void load_angles(Angles &t, const AppendArgs &A, int u, int pos)
+{
+    if (u * 16 < A.rot) {
+        const int64_t at = (int64_t)pos * (A.rot / 2) + u * 8;
+        load8(A.cos + at, t.c);
+        load8(A.sin + at, t.s);
+    }
+}
+
+__device__ __forceinline__ void rotate_row(Row16 &r, const AppendArgs &A, int u, const Angles &t)
 {
     if (u * 16 >= A.rot)
         return;
-    float c[8], s[8];
-    const int64_t at = (int64_t)pos * (A.rot / 2) + u * 8;
-    load8(A.cos + at, c);
-    load8(A.sin + at, s);
     if (A.interleaved) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            rotate_pair(r.a[2 * i], r.a[2 * i + 1], c[i], s[i]);
-            rotate_pair(r.b[2 * i], r.b[2 * i + 1], c[4 + i], s[4 + i]);
+            rotate_pair(r.a[2 * i], r.a[2 * i + 1], t.c[i], t.s[i]);
+            rotate_pair(r.b[2 * i], r.b[2 * i + 1], t.c[4 + i], t.s[4 + i]);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            rotate_pair(r.a[i], r.b[i], c[i], s[i]);
+            rotate_pair(r.a[i], r.b[i], t.c[i], t.s[i]);
     }
 }
 
@@ -138,92 +169,116 @@ __device__ __forceinline__ float finite_abs(float v, bool &bad)
     return ok ? m : 0.0f;
 }
 
-template <typename T, int NT, int PASSES>
-__global__ void __launch_bounds__(NT) append_kernel(const __grid_constant__ AppendArgs A,
-                                                    unsigned n_blocks, unsigned cache_ctas,
-                                                    unsigned q_ctas)
+// FEW: a warp per page, head and K or V (a page gets at most four tokens), eight of them per CTA; otherwise a
+// CTA each. HPT: q heads per thread, which share the token's angles.
+template <typename T, int NT, int PASSES, bool FEW, int HPT>
+__global__ void __launch_bounds__(NT, 1024 / NT) append_kernel(const __grid_constant__ AppendArgs A, unsigned n_blocks,
+                                                    unsigned cache_items, unsigned cache_ctas, unsigned q_ctas)
 {
+    constexpr int kGroup = FEW ? 32 : NT, kTok = kGroup / 8;   // threads of a group, tokens per pass
     const Batch &B = A.b;
-    const int tid = threadIdx.x, u = tid & 7, r = tid >> 3;
-    unsigned item = blockIdx.x;
+    const int tid = threadIdx.x, u = tid & 7;
     int ca, cb;
     pieces(u, A.rot, A.interleaved, ca, cb);
+    wait_previous_grid();
+    allow_next_grid();
 
-    if (item >= cache_ctas) {   // ---- rotate q
-        item -= cache_ctas;
-        const int b = (int)(item / q_ctas), chunk = (int)(item % q_ctas);
+    if (blockIdx.x >= cache_ctas) {   // ---- rotate q
+        const unsigned item = blockIdx.x - cache_ctas;
+        const int b = (int)(item / q_ctas), r = (int)(item % q_ctas) * (NT / 8) + (tid >> 3);
+        const int groups = (B.Hq + HPT - 1) / HPT, tok = r / groups, h0 = (r - tok * groups) * HPT;
         const Seq s = load_seq(B, b);
-        const int64_t rows = (int64_t)s.n * B.Hq;
-        const T *q = static_cast<const T *>(A.q);
-        __nv_bfloat16 *qo = static_cast<__nv_bfloat16 *>(A.q_out);
-        if (s.L > A.n_positions && A.rot > 0)
-            return;             // the cache blocks report it
-        Row16 x[2];
+        if (tok >= s.n || (s.L > A.n_positions && A.rot > 0))
+            return;                   // the cache groups report positions past the table
+        const T *src = static_cast<const T *>(A.q) + (int64_t)(s.row0 + tok) * A.q_stride + h0 * kHd;
+        __nv_bfloat16 *dst =
+            static_cast<__nv_bfloat16 *>(A.q_out) + ((int64_t)(s.row0 + tok) * B.Hq + h0) * kHd;
+        Angles t;
+        load_angles(t, A, u, max(s.L - s.n + tok, 0));
+        constexpr int kAtOnce = HPT < 2 ? HPT : 2;
+#pragma unroll 1
+        for (int i0 = 0; i0 < HPT && h0 + i0 < B.Hq; i0 += kAtOnce) {
+            Raw8<T> x[kAtOnce][2];
 #pragma unroll
-        for (int i = 0; i < kQRows / (NT / 8); ++i) {
-            const int64_t row = (int64_t)chunk * kQRows + i * (NT / 8) + r;
-            if (row >= rows)
-                break;
-            const int tok = (int)(row / B.Hq), h = (int)(row - (int64_t)tok * B.Hq);
-            const T *src = q + (int64_t)(s.row0 + tok) * A.q_stride + h * kHd;
-            Row16 &y = x[i & 1];
-            load8(src + ca, y.a);
-            load8(src + cb, y.b);
-            rotate_row(y, A, u, max(s.L - s.n + tok, 0));
-            __nv_bfloat16 *dst = qo + ((int64_t)(s.row0 + tok) * B.Hq + h) * kHd;
-            *reinterpret_cast<uint4 *>(dst + ca) = pack_bf16(y.a);
-            *reinterpret_cast<uint4 *>(dst + cb) = pack_bf16(y.b);
+            for (int i = 0; i < kAtOnce; ++i)
+                if (h0 + i0 + i < B.Hq) {
+                    x[i][0].load(src + (i0 + i) * kHd + ca);
+                    x[i][1].load(src + (i0 + i) * kHd + cb);
+                }
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i)
+                if (h0 + i0 + i < B.Hq) {
+                    Row16 y;
+                    x[i][0].get(y.a);
+                    x[i][1].get(y.b);
+                    rotate_row(y, A, u, t);
+                    *reinterpret_cast<uint4 *>(dst + (i0 + i) * kHd + ca) = pack_bf16(y.a);
+                    *reinterpret_cast<uint4 *>(dst + (i0 + i) * kHd + cb) = pack_bf16(y.b);
+                }
         }
         return;
     }
 
     // ---- one page of K or V of one head
+    const int g = FEW ? tid & 31 : tid, r = g >> 3;
+    unsigned item = FEW ? blockIdx.x * (NT / 32) + (tid >> 5) : blockIdx.x;
+    if (item >= cache_items)
+        return;
     const int which = (int)(item % 2), h = (int)(item / 2 % (unsigned)B.Hkv);
     item /= 2 * (unsigned)B.Hkv;
     const int b = (int)(item / n_blocks), j = (int)(item % n_blocks);
     const Seq s = load_seq(B, b);
     if (!s.ok || (s.L > A.n_positions && A.rot > 0 && s.n > 0)) {
-        if (tid == 0)
+        if (g == 0)
             atomicOr(&g_append_error, kErrMeta);
         return;
     }
+    const int page_shift = 31 - __clz(B.P);
     const int p_first = max(s.L - s.n, 0);          // first position written
-    const int blk = p_first / B.P + j;
-    const int p0 = max(p_first, blk * B.P);         // this block's new positions [p0, p1)
-    const int p1 = min(s.L, (blk + 1) * B.P);
+    const int blk = (p_first >> page_shift) + j;
+    const int p0 = max(p_first, blk << page_shift); // this page's new positions [p0, p1)
+    const int p1 = min(s.L, (blk + 1) << page_shift);
     if (s.n == 0 || p0 >= p1)
         return;
     const int page = __ldg(B.page_table + (int64_t)b * B.max_pages + blk);
-    if (page < 0 || page >= B.n_pages) {
-        if (tid == 0)
-            atomicOr(&g_append_error, kErrMeta);
-        return;
-    }
     const T *src = static_cast<const T *>(which ? A.v : A.k);
     const int64_t stride = which ? A.v_stride : A.k_stride;
-    const int64_t head = (int64_t)page * B.Hkv + h;
-    uint8_t *codes = (which ? B.v : B.k) + head * B.P * kHd;
-    float *scale = (which ? B.v_scale : B.k_scale) + head;
     const int first_row = s.row0 + s.n - s.L;       // token row of position 0
 
+    Raw8<T> raw[PASSES][2];
     Row16 x[PASSES];
     float amax = 0.0f;
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
-        const int pos = p0 + i * (NT / 8) + r;
+        const int pos = p0 + i * kTok + r;
         if (pos < p1) {
             const T *row = src + (int64_t)(first_row + pos) * stride + h * kHd;
-            load8(row + ca, x[i].a);
-            load8(row + cb, x[i].b);
+            raw[i][0].load(row + ca);
+            raw[i][1].load(row + cb);
         }
     }
+    if (page < 0 || page >= B.n_pages) {
+        if (g == 0)
+            atomicOr(&g_append_error, kErrMeta);
+        return;
+    }
+    const int64_t head = (int64_t)page * B.Hkv + h;
+    uint8_t *codes = (which ? B.v : B.k) + head * B.P * kHd;
+    float *scale = (which ? B.v_scale : B.k_scale) + head;
+    const bool fresh = p0 == blk << page_shift;
+    const float s_old = fresh ? 0.0f : *scale;
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
-        const int pos = p0 + i * (NT / 8) + r;
+        const int pos = p0 + i * kTok + r;
         if (pos < p1) {
-            if (!which)
-                rotate_row(x[i], A, u, pos);
+            raw[i][0].get(x[i].a);
+            raw[i][1].get(x[i].b);
+            if (!which) {
+                Angles t;
+                load_angles(t, A, u, pos);
+                rotate_row(x[i], A, u, t);
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 amax = fmaxf(amax, finite_abs(x[i].a[e], bad));
@@ -236,23 +291,26 @@ __global__ void __launch_bounds__(NT) append_kernel(const __grid_constant__ Appe
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1)
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
-    __shared__ float warp_max[NT / 32];
-    if ((tid & 31) == 0)
-        warp_max[tid >> 5] = amax;
-    const bool fresh = p0 == blk * B.P;
-    const float s_old = fresh ? 0.0f : *scale;
-    __syncthreads();
+    if (!FEW) {
+        __shared__ float warp_max[NT / 32];
+        if ((tid & 31) == 0)
+            warp_max[tid >> 5] = amax;
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < NT / 32; ++i)
-        amax = fmaxf(amax, warp_max[i]);
+        for (int i = 0; i < NT / 32; ++i)
+            amax = fmaxf(amax, warp_max[i]);
+    } else {
+        __syncwarp();
+    }
     const float s_new = fmaxf(s_old, pow2_scale(amax));
     const float inv = __frcp_rn(s_new);             // exact: s_new is a power of two
-    if (tid == 0)
+    if (g == 0)
         *scale = s_new;                             // every thread has read s_old
     if (!fresh && s_new > s_old) {                  // the page's other codes move to the new scale
         const float ratio = s_old * inv;
-        const int lo = p0 - blk * B.P, hi = p1 - blk * B.P;
-        for (int c = tid; c < B.P * kHd / 16; c += NT) {
+        const int lo = p0 - (blk << page_shift), hi = p1 - (blk << page_shift);
+#pragma unroll 1
+        for (int c = g; c < B.P * kHd / 16; c += kGroup) {
             const int slot = c >> 3;
             if (slot >= lo && slot < hi)
                 continue;
@@ -268,7 +326,7 @@ __global__ void __launch_bounds__(NT) append_kernel(const __grid_constant__ Appe
     }
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
-        const int pos = p0 + i * (NT / 8) + r;
+        const int pos = p0 + i * kTok + r;
         if (pos < p1) {
             float *a = x[i].a, *c = x[i].b;
 #pragma unroll
@@ -276,7 +334,7 @@ __global__ void __launch_bounds__(NT) append_kernel(const __grid_constant__ Appe
                 a[e] = a[e] == a[e] ? a[e] * inv : 0.0f;   // NaN is held as 0
                 c[e] = c[e] == c[e] ? c[e] * inv : 0.0f;
             }
-            uint8_t *dst = codes + (pos - blk * B.P) * kHd;
+            uint8_t *dst = codes + (pos - (blk << page_shift)) * kHd;
             *reinterpret_cast<uint2 *>(dst + ca) =
                 make_uint2(codes4(a[0], a[1], a[2], a[3]), codes4(a[4], a[5], a[6], a[7]));
             *reinterpret_cast<uint2 *>(dst + cb) =
@@ -285,26 +343,44 @@ __global__ void __launch_bounds__(NT) append_kernel(const __grid_constant__ Appe
     }
 }
 
+template <typename T, int NT, int PASSES, bool FEW, int HPT>
+static cudaError_t launch_form(const AppendArgs &a, cudaStream_t s)
+{
+    const Batch &B = a.b;
+    // a call of n tokens touches at most this many pages of a sequence
+    const int64_t n_blocks = ((int64_t)B.max_q + 2 * B.P - 2) / B.P;
+    const int64_t items = (int64_t)B.n_seq * n_blocks * B.Hkv * 2;
+    const int64_t cache_ctas = FEW ? (items + NT / 32 - 1) / (NT / 32) : items;
+    const int64_t groups = (B.Hq + HPT - 1) / HPT;
+    const int64_t q_ctas = a.q ? (B.max_q * groups + NT / 8 - 1) / (NT / 8) : 0;
+    const int64_t ctas = cache_ctas + (int64_t)B.n_seq * q_ctas;
+    if (items > 0x7fffffff || ctas > 0x7fffffff)
+        return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(NT);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, append_kernel<T, NT, PASSES, FEW, HPT>, a, (unsigned)n_blocks, (unsigned)items,
+                              (unsigned)cache_ctas, (unsigned)q_ctas);
+}
+
 template <typename T>
 static cudaError_t launch_typed(const AppendArgs &a, cudaStream_t s)
 {
     const Batch &B = a.b;
-    // a call of n tokens touches at most this many pages of a sequence
-    const int n_blocks = (int)(((int64_t)B.max_q + 2 * B.P - 2) / B.P);
-    const int64_t cache_ctas = (int64_t)B.n_seq * n_blocks * B.Hkv * 2;
-    const int q_ctas = a.q ? (int)(((int64_t)B.max_q * B.Hq + kQRows - 1) / kQRows) : 0;
-    const int64_t ctas = cache_ctas + (int64_t)B.n_seq * q_ctas;
-    if (ctas > 0x7fffffff)
-        return cudaErrorInvalidConfiguration;
-    const dim3 grid((unsigned)ctas);
-    const unsigned nb = (unsigned)n_blocks, nc = (unsigned)cache_ctas, nq = (unsigned)q_ctas;
+    if (B.max_q <= 4)
+        return launch_form<T, 256, 1, true, 1>(a, s);
     switch (B.P) {
-    case 16: append_kernel<T, 128, 1><<<grid, 128, 0, s>>>(a, nb, nc, nq); break;
-    case 32: append_kernel<T, 256, 1><<<grid, 256, 0, s>>>(a, nb, nc, nq); break;
-    case 64: append_kernel<T, 256, 2><<<grid, 256, 0, s>>>(a, nb, nc, nq); break;
-    default: append_kernel<T, 256, 4><<<grid, 256, 0, s>>>(a, nb, nc, nq); break;
+    case 16: return launch_form<T, 128, 1, false, 4>(a, s);
+    case 32: return launch_form<T, 256, 1, false, 4>(a, s);
+    case 64: return launch_form<T, 256, 2, false, 4>(a, s);
+    default: return launch_form<T, 512, 2, false, 4>(a, s);
     }
-    return cudaGetLastError();
 }
 
 cudaError_t launch_append(const AppendArgs &a, bool bf16, cudaStream_t s)
