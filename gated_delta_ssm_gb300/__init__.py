@@ -333,9 +333,7 @@ def _dtype(t) -> int:
 def _stream(stream) -> int | None:
     if stream is None:
         import torch
-        # the current stream's handle without building a Stream object (3 us on the Arm host)
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -533,13 +531,19 @@ def verify_commit_kn(state, conv_state, state_snap, conv_snap, n_accept, dims: D
 # the attributes that cost least.
 _torch = None
 _BF16_DT = _ACT_DT = _I32_DT = ()
+_current_device = _raw_stream = None
 
 
 def _load_torch():
-    global _torch, _BF16_DT, _ACT_DT, _I32_DT
+    global _torch, _BF16_DT, _ACT_DT, _I32_DT, _current_device, _raw_stream
     if _torch is None:
         import torch
         _BF16_DT, _ACT_DT, _I32_DT = (torch.bfloat16,), (torch.float32, torch.bfloat16), (torch.int32,)
+        if torch.cuda.is_available():
+            _current_device = torch.cuda.current_device
+            # the current stream's handle without building a Stream object (3 us on the Arm host)
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                  lambda dev: torch.cuda.current_stream(dev).cuda_stream)
         _torch = torch
     return _torch
 
@@ -595,10 +599,12 @@ def _counts(t, name: str, n: int, dev: int) -> int | None:
 def _device_and_stream(stream) -> tuple:
     """(index of the current CUDA device, stream handle); the device is -2 where there is none, which no
     tensor's checks pass."""
-    t = _torch or _load_torch()
-    if not t.cuda.is_available():
+    if _torch is None:
+        _load_torch()
+    if _current_device is None:
         return -2, None
-    return t.cuda.current_device(), _stream(stream)
+    dev = _current_device()
+    return dev, _raw_stream(dev) if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def attn_append(q, k, v, cache: KvCache, q_start, kv_len, rope: Rope, q_out, dims: AttnDims, stream=None):
