@@ -41,6 +41,7 @@ static __device__ int g_attn_decode_error;
 namespace {
 
 constexpr int kOver = 1;     // what a block costs besides its tiles, in tiles
+constexpr int kWhole = 3;    // most tiles of blocks that are not worth splitting
 constexpr float kNoRef = -1e30f;   // below every reference, and finite: 2^(-inf - kNoRef) is 0
 
 template <int NR>            // rows, padded
@@ -189,7 +190,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
     wait_previous_grid();
     Share share = {};
     if (B.n_seq > kFewSeqs)
-        share = find_share<kMaxDecodeRows, kOver>(A, sh.share, tid, kThreads, [] { __syncthreads(); });
+        share = find_share<kMaxDecodeRows, kOver, kWhole>(A, sh.share, tid, kThreads, [] { __syncthreads(); });
     PartMeta *const meta = reinterpret_cast<PartMeta *>(A.ws);
     float *const parts = part_slots(A.ws, gridDim.x);
     if (tid == kThreads - 128)   // the thread that may describe a block later
@@ -369,7 +370,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
         }
     } else if (warp == 3) {
         if (B.n_seq <= kFewSeqs)
-            share = find_share<kMaxDecodeRows, kOver>(A, sh.share, lane, 32, [] { __syncwarp(); });
+            share = find_share<kMaxDecodeRows, kOver, kWhole>(A, sh.share, lane, 32, [] { __syncwarp(); });
         walk_share<kMaxDecodeRows, kOver>(A, share, sh.ring, wait);
         clear_empty(A, &g_attn_decode_error);
     } else if (warp < 4 + 4 * C::kWgs) {
@@ -655,7 +656,7 @@ int row_pad(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 int most_ctas(int rows, int sms) { return sms * (row_pad(rows) == 16 ? Cfg<16>::kCtas : 1); }
 
 template <int NR>
-cudaError_t launch_rows(const AttnArgs &a, int grid, cudaStream_t s)
+cudaError_t launch_rows(const AttnArgs &a, int grid, bool may_split, cudaStream_t s)
 {
     CUtensorMap mk, mv;
     if (!encode_cache_map(&mk, a.b, a.b.k) || !encode_cache_map(&mv, a.b, a.b.v))
@@ -676,7 +677,7 @@ cudaError_t launch_rows(const AttnArgs &a, int grid, cudaStream_t s)
     cfg.numAttrs = 1;
     if ((e = cudaLaunchKernelEx(&cfg, attn_decode_kernel<NR>, a, mk, mv)) != cudaSuccess)
         return e;
-    return launch_join(a, grid, a.b.G * a.b.max_q, s);
+    return may_split ? launch_join(a, grid, a.b.G * a.b.max_q, s) : cudaSuccess;
 }
 
 }  // namespace
@@ -695,12 +696,15 @@ cudaError_t launch_decode(const AttnArgs &args, cudaStream_t s)
     const int rows = b.G * b.max_q, most = most_ctas(rows, a.sm_count);
     if (most_units(b, kMaxDecodeRows, kOver) > 2e9)
         return cudaErrorInvalidConfiguration;
-    const int64_t units = (((int64_t)b.max_pages * b.P + kTile - 1) / kTile + kOver) * b.n_seq * b.Hkv;
+    const int64_t tiles = ((int64_t)b.max_pages * b.P + kTile - 1) / kTile, blocks = (int64_t)b.n_seq * b.Hkv;
+    const int64_t units = (tiles + kOver) * blocks;
     const int grid = (int)(units < most ? units : most);
+    // the kernel decides by the lengths; where the page table's width decides already, nothing is ever joined
+    const bool may_split = tiles > kWhole || blocks > grid || b.n_seq > kFewSeqs;
     switch (row_pad(rows)) {
-    case 16: return launch_rows<16>(a, grid, s);
-    case 32: return launch_rows<32>(a, grid, s);
-    default: return launch_rows<64>(a, grid, s);
+    case 16: return launch_rows<16>(a, grid, may_split, s);
+    case 32: return launch_rows<32>(a, grid, may_split, s);
+    default: return launch_rows<64>(a, grid, may_split, s);
     }
 }
 

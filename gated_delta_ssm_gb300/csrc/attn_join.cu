@@ -27,16 +27,15 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
         return;
     const Seq s = load_seq(B, m.b);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int i = blockIdx.y * kPerCta + warp / SPLIT, piece = warp % SPLIT;
-    const int r = m.row0 + i, n = m.last_cta - (int)blockIdx.x + 1;
-    const bool live = i < rows && r < s.n * B.G;
+    const int piece = warp % SPLIT, n = m.last_cta - (int)blockIdx.x + 1;
+    const int live_rows = min(rows, s.n * B.G - m.row0);
     const size_t size = (size_t)rows * kPartRow;
-    const float *own = part_slots(A.ws, gridDim.x) + (size_t)(2 * blockIdx.x) * size + (size_t)i * kPartRow;
-    auto part = [&](int c) { return own + (size_t)(c == 0 ? 1 : 2 * c) * size; };
-    float l = 0.0f;
-    float4 o = make_float4(0, 0, 0, 0);
-    if (live) {
-        float big = -INFINITY;
+    const float *const own = part_slots(A.ws, gridDim.x) + (size_t)(2 * blockIdx.x) * size;
+#pragma unroll 1
+    for (int i = blockIdx.y * kPerCta + warp / SPLIT; i < live_rows; i += gridDim.y * kPerCta) {
+        auto part = [&](int c) { return own + (size_t)(c == 0 ? 1 : 2 * c) * size + (size_t)i * kPartRow; };
+        float l = 0.0f, big = -INFINITY;
+        float4 o = make_float4(0, 0, 0, 0);
         for (int c = lane; c < n; c += 32)
             big = fmaxf(big, part(c)[kHd + 1]);
 #pragma unroll
@@ -54,30 +53,29 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
             o.z = fmaf(x.z, b, o.z);
             o.w = fmaf(x.w, b, o.w);
         }
-    }
-    if (SPLIT > 1) {
-        sum[warp][lane] = o;
-        if (lane == 0)
-            sum_l[warp] = l;
-        __syncthreads();
-        if (piece != 0)
-            return;
+        if (SPLIT > 1) {   // the CTA's warps are at the same row
+            __syncthreads();
+            sum[warp][lane] = o;
+            if (lane == 0)
+                sum_l[warp] = l;
+            __syncthreads();
+            if (piece != 0)
+                continue;
 #pragma unroll
-        for (int k = 1; k < SPLIT; ++k) {
-            const float4 x = sum[warp + k][lane];
-            l += sum_l[warp + k];
-            o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+            for (int k = 1; k < SPLIT; ++k) {
+                const float4 x = sum[warp + k][lane];
+                l += sum_l[warp + k];
+                o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+            }
         }
+        const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
+        const int r = m.row0 + i, tok = div_G(B, r), g = r - tok * B.G;
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+        reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(A.out) +
+                                  ((int64_t)(s.row0 + tok) * B.Hq + m.h * B.G + g) * kHd)[lane] =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
     }
-    if (!live)
-        return;
-    const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
-    const int tok = r / B.G, g = r - tok * B.G;
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv);
-    const __nv_bfloat162 hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-    reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(A.out) +
-                              ((int64_t)(s.row0 + tok) * B.Hq + m.h * B.G + g) * kHd)[lane] =
-        make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
 }
 
 // A decode call's few rows can span every CTA, so four warps share a row; a prefill block has 256 rows of
@@ -89,7 +87,8 @@ cudaError_t launch_join(const AttnArgs &a, int grid, int rows, cudaStream_t s)
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(grid, few ? rows : (rows + 3) / 4);
+    // most CTAs find nothing to join: a grid of few keeps their launch short
+    cfg.gridDim = dim3(grid, few ? (rows < 8 ? rows : 8) : 8);
     cfg.blockDim = dim3(128);
     cfg.stream = s;
     cfg.attrs = attr;

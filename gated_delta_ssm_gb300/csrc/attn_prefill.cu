@@ -37,6 +37,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kRows = 256;                    // q rows per block
 constexpr int kOver = 6;                      // what a block costs besides its tiles, in tiles
+constexpr int kWhole = 8;                     // most tiles of blocks that are not worth splitting
 constexpr int kKs = 3, kVs = 2, kVb = 2;      // stages: K codes, V codes, V in bf16
 constexpr uint32_t kQAt = 0;                  // [A, B][hi, lo] 128 rows of 128 bytes
 constexpr uint32_t kKAt = kQAt + 4 * kTileBytes;
@@ -330,7 +331,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
     wait_previous_grid();
     Share share = {};
     if (B.n_seq > kFewSeqs)
-        share = find_share<kRows, kOver>(A, sh.share, tid, kThreads, [] { __syncthreads(); });
+        share = find_share<kRows, kOver, kWhole>(A, sh.share, tid, kThreads, [] { __syncthreads(); });
     PartMeta *const meta = reinterpret_cast<PartMeta *>(A.ws);
     float *const parts = part_slots(A.ws, gridDim.x);
     if (tid == 128)   // the thread that may describe a block later
@@ -479,7 +480,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
         __syncwarp();
     } else if (warp == 3) {
         if (B.n_seq <= kFewSeqs)
-            share = find_share<kRows, kOver>(A, sh.share, lane, 32, [] { __syncwarp(); });
+            share = find_share<kRows, kOver, kWhole>(A, sh.share, lane, 32, [] { __syncwarp(); });
         walk_share<kRows, kOver>(A, share, sh.ring, wait);
         clear_empty(A, &g_attn_prefill_error);
     } else if (warp < 12) {
@@ -761,7 +762,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
 }
 
 template <int CAP>
-cudaError_t launch_cap(const AttnArgs &a, int grid, cudaStream_t s)
+cudaError_t launch_cap(const AttnArgs &a, int grid, bool may_split, cudaStream_t s)
 {
     CUtensorMap mk, mv;
     if (!encode_cache_map(&mk, a.b, a.b.k) || !encode_cache_map(&mv, a.b, a.b.v))
@@ -782,7 +783,7 @@ cudaError_t launch_cap(const AttnArgs &a, int grid, cudaStream_t s)
     cfg.numAttrs = 1;
     if ((e = cudaLaunchKernelEx(&cfg, attn_prefill_kernel<CAP>, a, mk, mv)) != cudaSuccess)
         return e;
-    return launch_join(a, grid, kRows, s);
+    return may_split ? launch_join(a, grid, kRows, s) : cudaSuccess;
 }
 
 }  // namespace
@@ -801,10 +802,12 @@ cudaError_t launch_prefill(const AttnArgs &args, cudaStream_t s)
     const int64_t blocks = ((int64_t)b.max_q * b.G + kRows - 1) / kRows * b.Hkv * b.n_seq;
     const int64_t units = tiles >= a.sm_count || blocks >= a.sm_count ? a.sm_count : (tiles + kOver) * blocks;
     const int grid = (int)(units < a.sm_count ? units : a.sm_count);
+    // the kernel decides by the lengths; where the page table's width decides already, nothing is ever joined
+    const bool may_split = tiles > kWhole || blocks > grid || b.n_seq > kFewSeqs;
     switch (cap_mode(a.softcap)) {
-    case kNoCap: return launch_cap<kNoCap>(a, grid, s);
-    case kLowCap: return launch_cap<kLowCap>(a, grid, s);
-    default: return launch_cap<kAnyCap>(a, grid, s);
+    case kNoCap: return launch_cap<kNoCap>(a, grid, may_split, s);
+    case kLowCap: return launch_cap<kLowCap>(a, grid, may_split, s);
+    default: return launch_cap<kAnyCap>(a, grid, may_split, s);
     }
 }
 

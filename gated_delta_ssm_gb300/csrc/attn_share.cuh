@@ -53,6 +53,7 @@ struct ShareShared {
 struct Share {
     int n_cta, each, more;
     int first, count;                 // this CTA's first unit, and its units
+    bool split;                       // whether blocks may be split (a unit is a tile, or a whole block)
     int b, off, head_units;           // the first unit's sequence, its place there, units of one KV head there
     Seq s;
 };
@@ -86,30 +87,42 @@ __device__ __forceinline__ void block_keys(const AttnArgs &A, const Seq &s, int 
     hi = max(0, first + min(div_G(A.b, i * ROWS + ROWS - 1), s.n - 1));
 }
 
-template <int ROWS, int OVER>
-__device__ __forceinline__ int block_units(const AttnArgs &A, const Seq &s, int i)
+template <int ROWS>
+__device__ __forceinline__ int block_tiles(const AttnArgs &A, const Seq &s, int i)
 {
     int lo, hi;
     block_keys<ROWS>(A, s, i, lo, hi);
-    return hi / kTile - lo / kTile + 1 + OVER;
+    return hi / kTile - lo / kTile + 1;
 }
 
-// Units of one KV head of a sequence: blocks from, from + step, ..
+// A block's units: its tiles and OVER, or one where blocks are not split.
 template <int ROWS, int OVER>
-__device__ __forceinline__ int head_units(const AttnArgs &A, int b, int from, int step)
+__device__ __forceinline__ int block_units(const AttnArgs &A, const Seq &s, int i, bool split)
+{
+    return split ? block_tiles<ROWS>(A, s, i) + OVER : 1;
+}
+
+// Tiles of one KV head of a sequence, of blocks from, from + step, ..; their number and the longest's tiles are
+// added to `blocks` and `longest`.
+template <int ROWS>
+__device__ __forceinline__ int head_tiles(const AttnArgs &A, int b, int from, int step, int &blocks, int &longest)
 {
     const Seq s = load_seq(A.b, b);
     const int n = blocks_of<ROWS>(A.b, s);
     int u = 0;
 #pragma unroll 1
-    for (int i = from; i < n; i += step)
-        u += block_units<ROWS, OVER>(A, s, i);
+    for (int i = from; i < n; i += step) {
+        const int t = block_tiles<ROWS>(A, s, i);
+        u += t;
+        longest = max(longest, t);
+        ++blocks;
+    }
     return u;
 }
 
 // Count the batch and find where this CTA's share begins, by `threads` threads of which this is number tid
 // (whole warps). sync joins them.
-template <int ROWS, int OVER, int THREADS, typename Y>
+template <int ROWS, int OVER, int WHOLE, int THREADS, typename Y>
 __device__ __forceinline__ Share find_share(const AttnArgs &A, ShareShared<THREADS> &sh, int tid, int threads, Y sync)
 {
     const Batch &B = A.b;
@@ -121,12 +134,28 @@ __device__ __forceinline__ Share find_share(const AttnArgs &A, ShareShared<THREA
     const int per = g > 1 ? 1 : (B.n_seq + threads - 1) / threads;
     const int first_b = (tid / g) * per, sub = tid % g;
     int mine = 0;
+    int blocks = 0, longest = 0;
 #pragma unroll 2
     for (int i = 0; i < per; ++i)
         if (first_b + i < B.n_seq)
-            mine += head_units<ROWS, OVER>(A, first_b + i, sub, g);
-    for (int m = 1; m < g; m <<= 1)
+            mine += head_tiles<ROWS>(A, first_b + i, sub, g, blocks, longest);
+    for (int m = 1; m < g; m <<= 1) {
         mine += __shfl_xor_sync(0xffffffffu, mine, m);
+        blocks += __shfl_xor_sync(0xffffffffu, blocks, m);
+    }
+    // Few short blocks go to a CTA each, whole: to split them would cost more in joining than it saves.
+    // (Counted by one warp only; a CTA-wide count is of more sequences than CTAs.)
+    bool split = true;
+    if (threads == 32) {
+        int all = sub == 0 ? blocks : 0;
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) {
+            all += __shfl_xor_sync(0xffffffffu, all, m);
+            longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, m));
+        }
+        split = longest > WHOLE || (int64_t)all * B.Hkv > gridDim.x;
+    }
+    mine = split ? mine + OVER * blocks : blocks;
     const int one_head = mine;
     mine = sub == 0 ? mine * B.Hkv : 0;
     int incl = mine;
@@ -159,7 +188,11 @@ __device__ __forceinline__ Share find_share(const AttnArgs &A, ShareShared<THREA
         int at = incl - mine;
 #pragma unroll 1
         for (int i = 0; i < per && first_b + i < B.n_seq; ++i) {
-            const int u = g > 1 ? one_head : head_units<ROWS, OVER>(A, first_b + i, 0, 1);
+            int n = 0, most = 0, u = one_head;
+            if (per > 1) {
+                u = head_tiles<ROWS>(A, first_b + i, 0, 1, n, most);
+                u = split ? u + OVER * n : n;
+            }
             if (r.first < at + u * B.Hkv) {
                 sh.start_b = first_b + i;
                 sh.start_off = r.first - at;
@@ -171,6 +204,7 @@ __device__ __forceinline__ Share find_share(const AttnArgs &A, ShareShared<THREA
         }
     }
     sync();
+    r.split = split;
     r.b = sh.start_b;
     r.off = sh.start_off;
     r.head_units = sh.head_units;
@@ -199,7 +233,7 @@ __device__ __forceinline__ void walk_share(const AttnArgs &A, const Share &r, Ri
         int u = 0;
 #pragma unroll 1
         for (int k = i0; k < i1; ++k)
-            u += block_units<ROWS, OVER>(A, s, k);
+            u += block_units<ROWS, OVER>(A, s, k, r.split);
         int upto = u;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
@@ -212,7 +246,7 @@ __device__ __forceinline__ void walk_share(const AttnArgs &A, const Share &r, Ri
         if (here)
 #pragma unroll 1
             for (i = i0; i < i1; ++i) {
-                const int k = block_units<ROWS, OVER>(A, s, i);
+                const int k = block_units<ROWS, OVER>(A, s, i, r.split);
                 if (off < at + k)
                     break;
                 at += k;
@@ -229,9 +263,9 @@ __device__ __forceinline__ void walk_share(const AttnArgs &A, const Share &r, Ri
         if (left > 0) {
             int lo, hi;
             block_keys<ROWS>(A, s, i, lo, hi);
-            const int all = hi / kTile - lo / kTile + 1, end = min(all + OVER, t + left);
-            const int t0 = max(0, t - OVER);
-            q.nt = max(0, end - OVER) - t0;
+            const int all = hi / kTile - lo / kTile + 1, units = r.split ? all + OVER : 1;
+            const int end = min(units, t + left), t0 = r.split ? max(0, t - OVER) : 0;
+            q.nt = r.split ? max(0, end - OVER) - t0 : all;
             q.kt = lo / kTile + t0;
             q.b = b, q.h = h, q.row0 = s.row0, q.n = s.n, q.first = s.L - s.n, q.lo = lo, q.hi = hi;
             q.blk = i * ROWS;
@@ -239,7 +273,7 @@ __device__ __forceinline__ void walk_share(const AttnArgs &A, const Share &r, Ri
             q.rem0 = q.blk - q.tok0 * B.G;
             q.begins = t0 == 0;
             q.whole = q.nt == all;
-            q.last_cta = share_of(r, unit + (all + OVER - t) - 1);
+            q.last_cta = share_of(r, unit + (units - t) - 1);
             left -= end - t;
             unit += end - t;
             t = 0;
