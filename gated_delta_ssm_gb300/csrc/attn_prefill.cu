@@ -6,12 +6,12 @@
 // S = Q K^T with the key codes read as the pages lie in shared memory and q as
 // two e4m3 numbers (q times a power of two is hi + lo exactly): two 8-bit
 // products at twice the 16-bit rate, so K is never converted. The softmax runs
-// online with a lazy reference m: weights are 2^(s - m) and m moves only when a
-// row's maximum exceeds it by 2^8, which bf16 weights and 32-bit sums hold
-// without loss; output rows are rescaled then. Weights are rounded to bf16 (as
-// many bits as the result has) and multiply V, converted exactly from codes to
-// bf16 with its power-of-two page scale, O += P V, accumulated in 32 bits in
-// tensor memory.
+// online without looking for maxima: weights are 2^(s - m) with a reference m
+// that starts at 0 and moves only when a tile's weights leave 2^-60 .. 2^60.
+// Weights and sums are floating numbers of 8 exponent bits, so the reference
+// costs range, not precision. Weights are rounded to bf16 (as many bits as the
+// result has) and multiply V, converted exactly from codes to bf16 with its
+// power-of-two page scale, O += P V, accumulated in 32 bits in tensor memory.
 //
 // Bound by the tensor core: 4 * 128 flops per visible (row, key). While it works
 // on one tile, the other tile's 128 threads turn scores into weights. The grid
@@ -45,9 +45,7 @@ constexpr uint32_t kVAt = kKAt + kKs * kTileBytes;
 constexpr uint32_t kBAt = kVAt + kVs * kTileBytes;
 constexpr uint32_t kEnd = kBAt + kVb * 2 * kTileBytes;
 constexpr uint32_t kTmemCols = 512;           // S of A, S of B, O of A, O of B: 128 each
-// The reference moves when a row's weights of one tile sum to more than this: weights and sums are floating
-// numbers of 8 exponent bits, so a reference that lags behind costs no precision, only range.
-constexpr float kSlack = 8.0f, kSlackSum = 65536.0f;   // 128 weights of at most 2^8 sum to 2^15
+constexpr float kMostSum = 0x1p60f, kLeastSum = 0x1p-60f;   // of weights against a reference that stays
 
 struct Shared {
     uint64_t k_full[kKs], k_free[kKs], v_full[kVs], v_free[kVs], b_full[kVb], b_free[kVb];
@@ -56,6 +54,7 @@ struct Shared {
     volatile int abort;
     ShareShared<kThreads> share;
     Ring ring;
+    Seg now[8];                // the segment that each warp of rows is at
     float f[2][128];           // |scale| log2 e / (power of two of the q row)
 };
 
@@ -134,13 +133,15 @@ __device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16])
                  :: "memory");
 }
 
-// Weights of a row that sees the whole tile, against the reference as it is: one pass, no maximum. They are
-// stored if every row of the warp stayed within 2^kSlack summed; otherwise the scores are left as they were
-// and the caller takes the form that moves the reference.
-template <typename F>
-__device__ __forceinline__ bool row_weights_once(uint32_t s_at, F factor, float ref, float &l)
+// Weights of a row against the reference as it is: one pass, no maximum. They are stored if every row of the
+// warp is within range; otherwise the scores are left as they were and the caller takes the form that moves the
+// reference. In range: the tile's weights sum to at most 2^60, and those of the row so far to at least 2^-60
+// where it has seen a key, so that what the 8 exponent bits of weights and sums cannot hold is below 2^-60 of
+// the row's total.
+template <bool WHOLE, typename M, typename F>
+__device__ __forceinline__ bool row_weights_once(uint32_t s_at, M mask_of, F factor, float ref, float &l)
 {
-    uint32_t x[2][16], y[64];
+    uint32_t x[2][16], y[64], mask = 0xffffffffu, seen = WHOLE ? 1u : 0u;
     uint64_t sum[2] = {0, 0};
     const uint64_t sub2 = pack2(-ref, -ref);
     tmem_get16(s_at, x[0]);
@@ -150,6 +151,10 @@ __device__ __forceinline__ bool row_weights_once(uint32_t s_at, F factor, float 
         tmem_wait16(v);
         if (c < 7)
             tmem_get16(s_at + 16 * (c + 1), x[(c + 1) & 1]);
+        if (!WHOLE && c % 2 == 0) {
+            mask = mask_of(c / 2);
+            seen |= mask;
+        }
         const float fk = factor(c);
         const uint64_t fk2 = pack2(fk, fk);
 #pragma unroll
@@ -158,13 +163,17 @@ __device__ __forceinline__ bool row_weights_once(uint32_t s_at, F factor, float 
             float2 z = unpack2(fma2(pack2(s0, s1), fk2, sub2));
             z.x = ex2(z.x);
             z.y = ex2(z.y);
+            if (!WHOLE) {
+                z.x = mask >> (16 * (c & 1) + e) & 1 ? z.x : 0.0f;
+                z.y = mask >> (16 * (c & 1) + e + 1) & 1 ? z.y : 0.0f;
+            }
             sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pack2(z.x, z.y));
             y[8 * c + e / 2] = pack_bf16x2(z.x, z.y);
         }
     }
     const float2 t = unpack2(add2(sum[0], sum[1]));
     const float add = t.x + t.y;
-    if (!__all_sync(0xffffffffu, add <= kSlackSum))
+    if (!__all_sync(0xffffffffu, add <= kMostSum && (l + add >= kLeastSum || seen == 0)))
         return false;
     l += add;
 #pragma unroll
@@ -493,10 +502,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
         const float cap2 = A.softcap * kLog2e, inv_cap2 = CAP == kAnyCap ? 1.0f / cap2 : 0.0f;
         const float f_scale = fabsf(A.scale) * kLog2e, sign = A.scale < 0.0f ? -1.0f : 1.0f;
         int c = 0;
-        // the segment whose rows are written next
-        Seg w = {};
-        int tok = 0, head = 0;
-        bool live = false;
+        Seg &w = sh.now[warp - 4];   // in shared memory: the loop over tiles has no registers to spare for it
         float ref = 0.0f, l = 0.0f;
 #pragma unroll 1
         for (int k = 0;; ++k) {
@@ -553,6 +559,8 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                 wait(sh.o_done[m], (c - 1) & 1);
                 tc::fence_after_sync();
                 const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
+                const int y = w.rem0 + x, dt = y * inv_G >> 16, tok = w.tok0 + dt, head = y - dt * G;
+                const bool live = tok < w.n, joined = !w.whole;
                 uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(A.out) +
                                                        ((int64_t)(w.row0 + tok) * B.Hq + w.h * G + head) * kHd);
                 float *part = parts + ((size_t)(2 * blockIdx.x + (w.begins ? 1 : 0)) * kRows + x) * kPartRow;
@@ -561,7 +569,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                     uint32_t v[32];
                     tmem_get32(o_at + 32 * q4, v);
                     tmem_wait32(v);
-                    if (!w.whole) {
+                    if (joined) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
                             reinterpret_cast<uint4 *>(part)[8 * q4 + e] =
@@ -578,7 +586,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                         }
                     }
                 }
-                if (!w.whole) {
+                if (joined) {
                     *reinterpret_cast<float2 *>(part + kHd) = make_float2(l, ref);
                     if (w.begins && x == 0)
                         meta[blockIdx.x] = {w.b, w.h, w.blk, w.last_cta, 1, {}};
@@ -587,39 +595,40 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
             }
             if (nx.nt == 0)
                 break;
-            w = nx;
-            const int y = w.rem0 + x, dt = y * inv_G >> 16;
-            tok = w.tok0 + dt;
-            head = y - dt * G;
-            live = tok < w.n;
-            const int limit = live ? w.first + tok : -1;   // last position the row sees
+            __syncwarp();
+            if (lane == 0)
+                w = nx;
+            __syncwarp();
+            const int tok = nx.tok0 + ((nx.rem0 + x) * inv_G >> 16);
+            const int limit = tok < nx.n ? nx.first + tok : -1;   // last position the row sees
             // positions of the tile's first and last row, for key tiles that all of its rows see whole
-            const int tok_a = w.tok0 + ((w.rem0 + m * 128) * inv_G >> 16);
-            const int tok_b = w.tok0 + ((w.rem0 + m * 128 + 127) * inv_G >> 16);
-            const int all_to = tok_b < w.n ? w.first + tok_a : -1, all_from = w.first + tok_b - A.window;
-            const int32_t *table = B.page_table + (int64_t)w.b * B.max_pages;
-            const int pg_lo = w.lo >> page_shift, pg_hi = w.hi >> page_shift;
+            const int tok_a = nx.tok0 + ((nx.rem0 + m * 128) * inv_G >> 16);
+            const int tok_b = nx.tok0 + ((nx.rem0 + m * 128 + 127) * inv_G >> 16);
+            const int all_to = tok_b < nx.n ? nx.first + tok_a : -1, all_from = nx.first + tok_b - A.window;
+            const int32_t *table = B.page_table + (int64_t)nx.b * B.max_pages;
+            const int pg_lo = nx.lo >> page_shift, pg_hi = nx.hi >> page_shift;
             // lane p: scale of the tile's page p; 0 marks a page the table does not have
             auto page_at = [&](int t) {
-                const int pg = (w.kt + t) * per_tile + lane;
-                return t < w.nt && lane < per_tile && pg >= pg_lo && pg <= pg_hi ? __ldg(table + pg) : -3;
+                const int pg = (nx.kt + t) * per_tile + lane;
+                return t < nx.nt && lane < per_tile && pg >= pg_lo && pg <= pg_hi ? __ldg(table + pg) : -3;
             };
             auto scale_at = [&](int p) {
                 return p == -3 ? 1.0f
-                               : p >= 0 && p < B.n_pages ? __ldg(B.k_scale + (int64_t)p * B.Hkv + w.h) : 0.0f;
+                               : p >= 0 && p < B.n_pages ? __ldg(B.k_scale + (int64_t)p * B.Hkv + nx.h) : 0.0f;
             };
             int p_far = page_at(1);
             float ks_next = scale_at(page_at(0));
             const float f = sh.f[m][row];
-            ref = CAP == kLowCap ? 0.0f : -INFINITY;
+            const int nt = nx.nt, kt = nx.kt;
+            ref = 0.0f;
             l = 0.0f;
 #pragma unroll 1
-            for (int t = 0; t < w.nt; ++t, ++c) {
+            for (int t = 0; t < nt; ++t, ++c) {
                 const float ks = ks_next;
                 ks_next = scale_at(p_far);
                 p_far = page_at(t + 2);
                 const uint32_t bad = __ballot_sync(0xffffffffu, ks == 0.0f);
-                const int j0 = (w.kt + t) * kTile;
+                const int j0 = (kt + t) * kTile;
                 const bool whole = j0 + kTile - 1 <= all_to && j0 > all_from && bad == 0;
                 auto factor = [&](int sixteenth) {   // of 16 columns
                     return f * __shfl_sync(0xffffffffu, ks, (16 * sixteenth) >> page_shift);
@@ -642,14 +651,15 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                     l += whole ? row_weights_capped<true>(s_at, mask_of, factor, cap2)
                                : row_weights_capped<false>(s_at, mask_of, factor, cap2);
                 } else {
-                    if (CAP == kAnyCap || !whole || !__all_sync(0xffffffffu, ref > -INFINITY) ||
-                        !row_weights_once(s_at, factor, ref, l)) {
+                    if (CAP == kAnyCap ||
+                        !(whole ? row_weights_once<true>(s_at, mask_of, factor, ref, l)
+                                : row_weights_once<false>(s_at, mask_of, factor, ref, l))) {
                         const float top = row_max<CAP>(s_at, mask_of, factor, cap2, inv_cap2);
-                        // the reference moves when a weight would pass 2^kSlack, or is the row's first
-                        const bool move = top > ref + kSlack || (ref == -INFINITY && top > ref);
+                        // up where a weight would pass 2^8, down to a row's first keys
+                        const bool move = top > ref + 8.0f || (l == 0.0f && top < ref && top > -INFINITY);
                         if (__any_sync(0xffffffffu, move)) {
                             const float to = move ? top : ref;
-                            const float a = move ? ex2(ref - to) : 1.0f;
+                            const float a = move && l > 0.0f ? ex2(ref - to) : 1.0f;   // l = 0: so is O
                             ref = to;
                             l *= a;
                             if (t > 0) {
@@ -667,7 +677,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                                 }
                             }
                         }
-                        l += row_weights<CAP>(s_at, mask_of, factor, ref == -INFINITY ? 0.0f : ref, cap2, inv_cap2);
+                        l += row_weights<CAP>(s_at, mask_of, factor, ref, cap2, inv_cap2);
                     }
                 }
                 tc::tmem_wait_st();
