@@ -49,7 +49,7 @@ constexpr float kMostSum = 0x1p60f, kLeastSum = 0x1p-60f;   // of weights agains
 
 struct Shared {
     uint64_t k_full[kKs], k_free[kKs], v_full[kVs], v_free[kVs], b_full[kVb], b_free[kVb];
-    uint64_t q_full[2], s_full[2], p_full[2], o_done[2], drain[2];
+    uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_half[2], o_done[2], drain[2];
     uint32_t tmem;
     volatile int abort;
     ShareShared<kThreads> share;
@@ -133,67 +133,108 @@ __device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16])
                  :: "memory");
 }
 
-// Weights of a row against the reference as it is: one pass, no maximum. They are stored if every row of the
-// warp is within range; otherwise the scores are left as they were and the caller takes the form that moves the
-// reference. In range: the tile's weights sum to at most 2^60, and those of the row so far to at least 2^-60
-// where it has seen a key, so that what the 8 exponent bits of weights and sums cannot hold is below 2^-60 of
-// the row's total.
-template <bool WHOLE, typename M, typename F>
-__device__ __forceinline__ bool row_weights_once(uint32_t s_at, M mask_of, F factor, float ref, float &l)
+// Which columns of the tile a row sees: [lo, hi], but for the pages in `bad` (bits).
+struct RowMask {
+    int lo, hi, page_shift;
+    uint32_t bad;
+    __device__ __forceinline__ uint32_t operator()(int q4) const   // bit e: column 32 q4 + e is visible
+    {
+        const int h = hi - 32 * q4, o = lo - 32 * q4;
+        uint32_t v = h >= 31 ? 0xffffffffu : h < 0 ? 0u : (2u << h) - 1u;
+        v &= o <= 0 ? 0xffffffffu : o > 31 ? 0u : 0xffffffffu << o;
+        if (bad >> ((32 * q4) >> page_shift) & 1)
+            v &= 0xffff0000u;
+        if (bad >> ((32 * q4 + 16) >> page_shift) & 1)
+            v &= 0x0000ffffu;
+        return v;
+    }
+};
+
+// What a score of 16 neighbouring columns is multiplied by: the row's factor and the page's scale.
+struct RowFactor {
+    float f, ks;               // ks of lane p: the tile's page p
+    int page_shift;
+    __device__ __forceinline__ float operator()(int sixteenth) const
+    {
+        return f * __shfl_sync(0xffffffffu, ks, (16 * sixteenth) >> page_shift);
+    }
+};
+
+// Sixteen columns' weights, as bf16 pairs, against a reference; adds them to sum and returns the columns seen.
+template <bool WHOLE>
+__device__ __forceinline__ uint32_t weights16(uint32_t (&v)[16], uint32_t *y, int c, const RowMask &mask_of,
+                                              const RowFactor &factor, uint64_t sub2, uint64_t (&sum)[2])
 {
-    uint32_t x[2][16], y[64], mask = 0xffffffffu, seen = WHOLE ? 1u : 0u;
-    uint64_t sum[2] = {0, 0};
-    const uint64_t sub2 = pack2(-ref, -ref);
+    const uint32_t mask = WHOLE ? 0xffffu : mask_of(c / 2) >> (16 * (c & 1)) & 0xffffu;
+    const float fk = factor(c);
+    const uint64_t fk2 = pack2(fk, fk);
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+        float2 z = unpack2(fma2(pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), fk2, sub2));
+        z.x = ex2(z.x);
+        z.y = ex2(z.y);
+        if (!WHOLE) {
+            z.x = mask >> e & 1 ? z.x : 0.0f;
+            z.y = mask >> (e + 1) & 1 ? z.y : 0.0f;
+        }
+        sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pack2(z.x, z.y));
+        y[e / 2] = pack_bf16x2(z.x, z.y);
+    }
+    return mask;
+}
+
+// Weights of a row against the reference as it is: one pass, no maximum. Each half of the tile (64 keys) is
+// stored if every row of the warp is within range; otherwise its scores are left as they were and slow(half)
+// takes the form that moves the reference. In range: the weights sum to at most 2^60, and those of the row so
+// far to at least 2^-60 where it has seen a key, so that what the 8 exponent bits of weights and sums cannot
+// hold is below 2^-60 of the row's total. first() is called once the first half's weights are in place.
+template <bool WHOLE, typename S, typename H>
+__device__ __forceinline__ void row_weights(uint32_t s_at, const RowMask &mask_of, const RowFactor &factor, float &ref,
+                                            float &l, S slow, H first)
+{
+    uint32_t x[2][16], y[32];
     tmem_get16(s_at, x[0]);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        uint32_t(&v)[16] = x[c & 1];
-        tmem_wait16(v);
-        if (c < 7)
-            tmem_get16(s_at + 16 * (c + 1), x[(c + 1) & 1]);
-        if (!WHOLE && c % 2 == 0) {
-            mask = mask_of(c / 2);
-            seen |= mask;
-        }
-        const float fk = factor(c);
-        const uint64_t fk2 = pack2(fk, fk);
+    for (int half = 0; half < 2; ++half) {
+        uint64_t sum[2] = {0, 0};
+        const uint64_t sub2 = pack2(-ref, -ref);
+        uint32_t seen = 0;
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-            const float s0 = __uint_as_float(v[e]), s1 = __uint_as_float(v[e + 1]);
-            float2 z = unpack2(fma2(pack2(s0, s1), fk2, sub2));
-            z.x = ex2(z.x);
-            z.y = ex2(z.y);
-            if (!WHOLE) {
-                z.x = mask >> (16 * (c & 1) + e) & 1 ? z.x : 0.0f;
-                z.y = mask >> (16 * (c & 1) + e + 1) & 1 ? z.y : 0.0f;
-            }
-            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pack2(z.x, z.y));
-            y[8 * c + e / 2] = pack_bf16x2(z.x, z.y);
+        for (int i = 0; i < 4; ++i) {
+            const int c = 4 * half + i;
+            uint32_t(&v)[16] = x[c & 1];
+            tmem_wait16(v);
+            if (c < 7)
+                tmem_get16(s_at + 16 * (c + 1), x[(c + 1) & 1]);
+            seen |= weights16<WHOLE>(v, y + 8 * i, c, mask_of, factor, sub2, sum);
+            if (c == 4)        // one step late: the store of the first half's weights has ended by itself
+                first();
+        }
+        const float2 t = unpack2(add2(sum[0], sum[1]));
+        const float add = t.x + t.y;
+        if (__all_sync(0xffffffffu, add <= kMostSum && (l + add >= kLeastSum || seen == 0))) {
+            l += add;
+            tc::tmem_st16u(s_at + 32 * half, *reinterpret_cast<uint32_t(*)[16]>(y));
+            tc::tmem_st16u(s_at + 32 * half + 16, *reinterpret_cast<uint32_t(*)[16]>(y + 16));
+        } else {
+            slow(half);
         }
     }
-    const float2 t = unpack2(add2(sum[0], sum[1]));
-    const float add = t.x + t.y;
-    if (!__all_sync(0xffffffffu, add <= kMostSum && (l + add >= kLeastSum || seen == 0)))
-        return false;
-    l += add;
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-        tc::tmem_st16u(s_at + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(y + 16 * c));
-    return true;
 }
 
 // Weights of a row whose scores are capped at no more than kMostCap: the weights themselves stay within the
 // range of the numbers that hold them, so no reference is needed, and no maximum. In base 2 the capped score is
 // c - 2 c / (1 + e^(2 s / cap)); its absolute error, c 2^-22, is far below a bf16 weight's rounding. One
 // reciprocal serves two keys: exponents are held to 60, where tanh is 1.
-template <bool WHOLE, typename M, typename F>
-__device__ __forceinline__ float row_weights_capped(uint32_t s_at, M mask_of, F factor, float c)
+template <bool WHOLE>
+__device__ __forceinline__ float half_weights_capped(uint32_t s_at, int half_tile, const RowMask &mask_of,
+                                                     const RowFactor &factor, float c)
 {
     uint64_t sum[2] = {0, 0};
     const uint64_t one = pack2(1.0f, 1.0f), c2 = pack2(c, c), m2c = pack2(-2.0f * c, -2.0f * c);
     const float f = 2.0f * kLog2e / c;    // factor() gives base-2 scores: 2 log2 e s / cap = (2 log2 e / c) (s log2 e)
 #pragma unroll 1
-    for (int q4 = 0; q4 < 4; ++q4) {
+    for (int q4 = 2 * half_tile; q4 < 2 * half_tile + 2; ++q4) {
         uint32_t v[32], y[16];
         tmem_get32(s_at + 32 * q4, v);
         tmem_wait32(v);
@@ -237,14 +278,15 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool have)
                  : "memory");
 }
 
-// The largest visible score of this thread's row of the tile (128 columns at s_at), -inf for none. The cap
-// is monotonic and factors are not negative, so each 16 columns' raw maximum stands for them.
-template <int CAP, typename M, typename F>
-__device__ __forceinline__ float row_max(uint32_t s_at, M mask_of, F factor, float cap2, float inv_cap2)
+// The largest visible score of this thread's row in half a tile, -inf for none. The cap is monotonic and
+// factors are not negative, so each 16 columns' raw maximum stands for them.
+template <int CAP>
+__device__ __forceinline__ float half_max(uint32_t s_at, int half_tile, const RowMask &mask_of, const RowFactor &factor,
+                                          float cap2, float inv_cap2)
 {
     float top = -INFINITY;
 #pragma unroll 1
-    for (int q4 = 0; q4 < 4; ++q4) {
+    for (int q4 = 2 * half_tile; q4 < 2 * half_tile + 2; ++q4) {
         uint32_t v[32];
         tmem_get32(s_at + 32 * q4, v);
         tmem_wait32(v);
@@ -265,15 +307,15 @@ __device__ __forceinline__ float row_max(uint32_t s_at, M mask_of, F factor, flo
     return top;
 }
 
-// Weights of the row, 2^(score - sub), as bf16 pairs over the scores' columns; returns their sum. Weights
+// Weights of half a tile, 2^(score - sub), as bf16 pairs over the scores' columns; returns their sum. Weights
 // of 32 keys take 16 columns, over scores already read.
-template <int CAP, typename M, typename F>
-__device__ __forceinline__ float row_weights(uint32_t s_at, M mask_of, F factor, float sub, float cap2,
-                                             float inv_cap2)
+template <int CAP>
+__device__ __forceinline__ float half_weights_at(uint32_t s_at, int half_tile, const RowMask &mask_of,
+                                                 const RowFactor &factor, float sub, float cap2, float inv_cap2)
 {
     float sum = 0.0f;
 #pragma unroll 1
-    for (int q4 = 0; q4 < 4; ++q4) {
+    for (int q4 = 2 * half_tile; q4 < 2 * half_tile + 2; ++q4) {
         uint32_t v[32], y[16];
         tmem_get32(s_at + 32 * q4, v);
         tmem_wait32(v);
@@ -299,6 +341,43 @@ __device__ __forceinline__ float row_weights(uint32_t s_at, M mask_of, F factor,
     return sum;
 }
 
+// Half a tile in the form that moves the reference: the maximum first. o_bar, where it is not 0, is the barrier
+// (and parity) behind which O holds what the row has summed so far. Returns the reference and the sum.
+// Not inlined: it is hardly ever run, and its four copies would crowd the loop that it stands in.
+template <int CAP>
+__device__ __noinline__ float2 slow_half(uint32_t s_at, uint32_t o_at, int half, RowMask mask_of, RowFactor factor,
+                                         float ref, float l, float cap2, float inv_cap2, uint32_t o_bar,
+                                         uint32_t o_parity, uint64_t lim, volatile int *abort)
+{
+    const float top = half_max<CAP>(s_at, half, mask_of, factor, cap2, inv_cap2);
+    // up where a weight would pass 2^8, down to a row's first keys
+    const bool move = top > ref + 8.0f || (l == 0.0f && top < ref && top > -INFINITY);
+    if (__any_sync(0xffffffffu, move)) {
+        const float to = move ? top : ref;
+        const float a = move && l > 0.0f ? ex2(ref - to) : 1.0f;   // l = 0: so is O
+        ref = to;
+        l *= a;
+        if (o_bar != 0) {
+            if (!wait_phase(o_bar, o_parity, lim, abort))
+                *abort = 1;
+            __syncwarp();
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int q4 = 0; q4 < 8; ++q4) {
+                uint32_t v[16];
+                tmem_get16(o_at + 16 * q4, v);
+                tmem_wait16(v);
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    v[e] = __float_as_uint(__uint_as_float(v[e]) * a);
+                tc::tmem_st16u(o_at + 16 * q4, v);
+            }
+        }
+    }
+    l += half_weights_at<CAP>(s_at, half, mask_of, factor, ref, cap2, inv_cap2);
+    return make_float2(ref, l);
+}
+
 template <int CAP>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ CUtensorMap map_k,
@@ -322,8 +401,8 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
         for (int i = 0; i < 2; ++i) {
             init(sh.q_full[i], 128);
             init(sh.s_full[i], 1);
-            init(sh.p_full[i], 128);
-            init(sh.o_done[i], 1);
+            init(sh.p_half[i], 128), init(sh.p_full[i], 128);
+            init(sh.o_half[i], 1), init(sh.o_done[i], 1);
             init(sh.drain[i], 1);
         }
         for (int i = 0; i < kRing; ++i)
@@ -451,14 +530,26 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
             if (j >= 0) {
                 const int vb = j % kVb;
                 wait(sh.b_full[vb], (j / kVb) & 1);
+                wait(sh.p_half[m], j & 1);
+                tc::fence_after_sync();
+                // 16 keys at a time: 8 columns of P, 2 KB of V; the first 64 while the others' weights form
+                const uint64_t v = tc::sdesc_sw128_mn(base + kBAt + vb * 2 * kTileBytes, kTileBytes, 1024);
+                if (leader) {
+                    if (!sh.abort) {
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            tc::mma_f16_ta(o_at, s_at + 8 * s, v + 128 * s, idesc_o, s > 0 || !begin);
+                    }
+                    tc::mma_commit(tc::smem_addr(&sh.o_half[m]));
+                }
+                __syncwarp();
                 wait(sh.p_full[m], j & 1);
                 tc::fence_after_sync();
                 if (leader) {
                     if (!sh.abort) {
-                        const uint64_t v = tc::sdesc_sw128_mn(base + kBAt + vb * 2 * kTileBytes, kTileBytes, 1024);
 #pragma unroll
-                        for (int s = 0; s < 8; ++s)   // 16 keys: 8 columns of P, 2 KB of V
-                            tc::mma_f16_ta(o_at, s_at + 8 * s, v + 128 * s, idesc_o, s > 0 || !begin);
+                        for (int s = 4; s < 8; ++s)
+                            tc::mma_f16_ta(o_at, s_at + 8 * s, v + 128 * s, idesc_o, 1);
                     }
                     if (more && !fresh)
                         issue_scores();
@@ -630,54 +721,37 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                 const uint32_t bad = __ballot_sync(0xffffffffu, ks == 0.0f);
                 const int j0 = (kt + t) * kTile;
                 const bool whole = j0 + kTile - 1 <= all_to && j0 > all_from && bad == 0;
-                auto factor = [&](int sixteenth) {   // of 16 columns
-                    return f * __shfl_sync(0xffffffffu, ks, (16 * sixteenth) >> page_shift);
-                };
                 wait(sh.s_full[m], c & 1);
                 tc::fence_after_sync();
-                const int hi = limit - j0, lo = limit - A.window + 1 - j0;   // visible columns [lo, hi]
-                // bit e: column 32 q4 + e is visible
-                auto mask_of = [&](int q4) {
-                    const int h = hi - 32 * q4, o = lo - 32 * q4;
-                    uint32_t v = h >= 31 ? 0xffffffffu : h < 0 ? 0u : (2u << h) - 1u;
-                    v &= o <= 0 ? 0xffffffffu : o > 31 ? 0u : 0xffffffffu << o;
-                    if (bad >> ((32 * q4) >> page_shift) & 1)
-                        v &= 0xffff0000u;
-                    if (bad >> ((32 * q4 + 16) >> page_shift) & 1)
-                        v &= 0x0000ffffu;
-                    return v;
+                const RowMask mask_of = {limit - A.window + 1 - j0, limit - j0, page_shift, bad};
+                const RowFactor factor = {f, ks, page_shift};
+                auto first = [&] {     // the first 64 keys' weights are there
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                    arrive(sh.p_half[m]);
                 };
-                if constexpr (CAP == kLowCap) {
-                    l += whole ? row_weights_capped<true>(s_at, mask_of, factor, cap2)
-                               : row_weights_capped<false>(s_at, mask_of, factor, cap2);
+                auto slow = [&](int half) {
+                    const uint32_t bar = half ? tc::smem_addr(&sh.o_half[m]) : t > 0 ? tc::smem_addr(&sh.o_done[m]) : 0u;
+                    const float2 r = slow_half<CAP>(s_at, o_at, half, mask_of, factor, ref, l, cap2, inv_cap2, bar,
+                                                    (half ? c : c - 1) & 1, lim, &sh.abort);
+                    ref = r.x;
+                    l = r.y;
+                };
+                if constexpr (CAP == kNoCap) {
+                    if (whole)
+                        row_weights<true>(s_at, mask_of, factor, ref, l, slow, first);
+                    else
+                        row_weights<false>(s_at, mask_of, factor, ref, l, slow, first);
                 } else {
-                    if (CAP == kAnyCap ||
-                        !(whole ? row_weights_once<true>(s_at, mask_of, factor, ref, l)
-                                : row_weights_once<false>(s_at, mask_of, factor, ref, l))) {
-                        const float top = row_max<CAP>(s_at, mask_of, factor, cap2, inv_cap2);
-                        // up where a weight would pass 2^8, down to a row's first keys
-                        const bool move = top > ref + 8.0f || (l == 0.0f && top < ref && top > -INFINITY);
-                        if (__any_sync(0xffffffffu, move)) {
-                            const float to = move ? top : ref;
-                            const float a = move && l > 0.0f ? ex2(ref - to) : 1.0f;   // l = 0: so is O
-                            ref = to;
-                            l *= a;
-                            if (t > 0) {
-                                wait(sh.o_done[m], (c - 1) & 1);
-                                tc::fence_after_sync();
 #pragma unroll 1
-                                for (int q4 = 0; q4 < 8; ++q4) {
-                                    uint32_t v[16];
-                                    tmem_get16(o_at + 16 * q4, v);
-                                    tmem_wait16(v);
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e)
-                                        v[e] = __float_as_uint(__uint_as_float(v[e]) * a);
-                                    tc::tmem_st16u(o_at + 16 * q4, v);
-                                }
-                            }
-                        }
-                        l += row_weights<CAP>(s_at, mask_of, factor, ref, cap2, inv_cap2);
+                    for (int half = 0; half < 2; ++half) {
+                        if constexpr (CAP == kAnyCap)
+                            slow(half);
+                        else
+                            l += whole ? half_weights_capped<true>(s_at, half, mask_of, factor, cap2)
+                                       : half_weights_capped<false>(s_at, half, mask_of, factor, cap2);
+                        if (half == 0)
+                            first();
                     }
                 }
                 tc::tmem_wait_st();
@@ -762,7 +836,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
             }
         }
     }
-    if (failed)
+    if (failed || sh.abort)
         atomicOr(&g_attn_prefill_error, kErrWait);
     tc::fence_before_sync();
     __syncthreads();
