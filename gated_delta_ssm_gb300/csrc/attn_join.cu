@@ -88,7 +88,7 @@ cudaError_t launch_join(const AttnArgs &a, int grid, int rows, cudaStream_t s)
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     // most CTAs find nothing to join: a grid of few keeps their launch short
-    cfg.gridDim = dim3(grid, few ? (rows < 8 ? rows : 8) : 8);
+    cfg.gridDim = dim3(grid, few ? (rows < 8 ? rows : 8) : 32);
     cfg.blockDim = dim3(128);
     cfg.stream = s;
     cfg.attrs = attr;

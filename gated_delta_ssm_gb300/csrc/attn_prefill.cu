@@ -47,6 +47,17 @@ constexpr uint32_t kEnd = kBAt + kVb * 2 * kTileBytes;
 constexpr uint32_t kTmemCols = 512;           // S of A, S of B, O of A, O of B: 128 each
 constexpr float kMostSum = 0x1p60f, kLeastSum = 0x1p-60f;   // of weights against a reference that stays
 
+template <int N>
+__device__ __forceinline__ void registers_up()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_down()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N));
+}
+
 struct Shared {
     uint64_t k_full[kKs], k_free[kKs], v_full[kVs], v_free[kVs], b_full[kVb], b_free[kVb];
     uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_half[2], o_done[2], drain[2];
@@ -444,147 +455,153 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
     };
     auto arrive = [&](const uint64_t &bar) { tc::mbar_arrive(tc::smem_addr(&bar)); };
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ pages to shared memory
-        int c = 0, issued = 0;
-        const int per_tile = kTile >> page_shift;
+    // Registers move to the two groups of warps that hold rows: 128 (88 + 160 + 160 + 96) of the 65,536 that the
+    // CTA starts with are 64,512.
+    if (warp < 4) {
+        registers_down<88>();
+        if (warp == 0) {
+            // ------------------------------------------------------------ pages to shared memory
+            int c = 0, issued = 0;
+            const int per_tile = kTile >> page_shift;
 #pragma unroll 1
-        for (int k = 0;; ++k) {
-            const Seg w = take_seg(sh.ring, k, wait);
-            if (w.nt == 0)
-                break;
-            const int32_t *table = B.page_table + (int64_t)w.b * B.max_pages;
-            const int pg_lo = w.lo >> page_shift, pg_hi = w.hi >> page_shift;
-            auto page_of = [&](int t) {   // this lane's page of the tile, -1: none wanted, -2: bad
-                const int pg = (w.kt + t) * per_tile + lane;
-                if (t >= w.nt || lane >= per_tile || pg < pg_lo || pg > pg_hi)
-                    return -1;
-                const int p = __ldg(table + pg);
-                return p >= 0 && p < B.n_pages ? p : -2;
+            for (int k = 0;; ++k) {
+                const Seg w = take_seg(sh.ring, k, wait);
+                if (w.nt == 0)
+                    break;
+                const int32_t *table = B.page_table + (int64_t)w.b * B.max_pages;
+                const int pg_lo = w.lo >> page_shift, pg_hi = w.hi >> page_shift;
+                auto page_of = [&](int t) {   // this lane's page of the tile, -1: none wanted, -2: bad
+                    const int pg = (w.kt + t) * per_tile + lane;
+                    if (t >= w.nt || lane >= per_tile || pg < pg_lo || pg > pg_hi)
+                        return -1;
+                    const int p = __ldg(table + pg);
+                    return p >= 0 && p < B.n_pages ? p : -2;
+                };
+                int page = page_of(0);
+#pragma unroll 1
+                for (int t = 0; t < w.nt; ++t, ++c) {
+                    const int next = page_of(t + 1);
+                    const bool have = page >= 0;
+                    if (page == -2)
+                        atomicOr(&g_attn_prefill_error, kErrMeta);
+                    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, have)) * B.P * kHd;
+#pragma unroll 1
+                    for (int part = 0; part < 2; ++part) {   // K, then V
+                        const int stages = part ? kVs : kKs, st = c % stages;
+                        if (c >= stages)
+                            wait(part ? sh.v_free[st] : sh.k_free[st], (c / stages - 1) & 1);
+                        if (__any_sync(0xffffffffu, sh.abort != 0))
+                            continue;
+                        const uint32_t bar = tc::smem_addr(part ? &sh.v_full[st] : &sh.k_full[st]);
+                        if (lane == 0)
+                            tc::mbar_expect_tx(bar, bytes);
+                        __syncwarp();
+                        if (have)
+                            copy_page(part ? &map_v : &map_k,
+                                      base + (part ? kVAt : kKAt) + st * kTileBytes + lane * B.P * kHd, bar,
+                                      page * B.Hkv + w.h);
+                        issued = 2 * c + part + 1;
+                    }
+                    page = next;
+                }
+            }
+            // after a wait that gave up: the copies in flight land before the CTA ends
+            for (int i = max(0, issued - 2 * kKs); i < issued && sh.abort; ++i) {
+                const int tile = i / 2, stages = i & 1 ? kVs : kKs;
+                if ((issued - 1 - i) / 2 < stages)
+                    tc::mbar_wait_ns(tc::smem_addr(i & 1 ? &sh.v_full[tile % stages] : &sh.k_full[tile % stages]),
+                                     (tile / stages) & 1, lim);
+            }
+        } else if (warp < 3) {
+            // ------------------------------------------------------------ products: warp 1 those of tile A, warp
+            // 2 those of B. A thread's products run in the order of their issue, so S of the next tile may be
+            // issued behind the product that reads P from the same columns.
+            const int m = warp - 1;
+            const bool leader = elect_one();
+            constexpr uint32_t idesc_s = idesc_e4m3(128, 128);
+            constexpr uint32_t idesc_o = tc::idesc_f16(128, 128) | 1u << 7 | 1u << 10 | tc::kIdescTransB;
+            const uint32_t s_at = tmem + m * 128, o_at = tmem + 256 + m * 128;
+            const uint64_t q = tc::sdesc_sw128(base + kQAt + 2 * m * kTileBytes);
+            int k = 0, c = 0, left = take_seg(sh.ring, 0, wait).nt;   // segment, tile, its tiles left: of the next scores
+            bool fresh = true, begin = true;  // whether that tile, and that of the next output, begins its segment
+            auto issue_scores = [&] {         // by one thread
+                const int ks = c % kKs;
+                if (!sh.abort) {
+                    const uint64_t kd = tc::sdesc_sw128(base + kKAt + ks * kTileBytes);
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)   // 32 bytes of the rows at a time
+                            mma_e4m3(s_at, q + part * (kTileBytes >> 4) + 2 * s, kd + 2 * s, idesc_s, part + s > 0);
+                }
+                tc::mma_commit(tc::smem_addr(&sh.s_full[m]));
+                tc::mma_commit(tc::smem_addr(&sh.k_free[ks]));
             };
-            int page = page_of(0);
 #pragma unroll 1
-            for (int t = 0; t < w.nt; ++t, ++c) {
-                const int next = page_of(t + 1);
-                const bool have = page >= 0;
-                if (page == -2)
-                    atomicOr(&g_attn_prefill_error, kErrMeta);
-                const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, have)) * B.P * kHd;
-#pragma unroll 1
-                for (int part = 0; part < 2; ++part) {   // K, then V
-                    const int stages = part ? kVs : kKs, st = c % stages;
-                    if (c >= stages)
-                        wait(part ? sh.v_free[st] : sh.k_free[st], (c / stages - 1) & 1);
-                    if (__any_sync(0xffffffffu, sh.abort != 0))
-                        continue;
-                    const uint32_t bar = tc::smem_addr(part ? &sh.v_full[st] : &sh.k_full[st]);
-                    if (lane == 0)
-                        tc::mbar_expect_tx(bar, bytes);
+            for (int j = -1; j < c; ++j) {    // output of tile j, scores of tile j + 1
+                const bool more = left > 0;
+                if (more)
+                    wait(sh.k_full[c % kKs], (c / kKs) & 1);
+                if (j >= 0) {
+                    const int vb = j % kVb;
+                    wait(sh.b_full[vb], (j / kVb) & 1);
+                    wait(sh.p_half[m], j & 1);
+                    tc::fence_after_sync();
+                    // 16 keys at a time: 8 columns of P, 2 KB of V; the first 64 while the others' weights form
+                    const uint64_t v = tc::sdesc_sw128_mn(base + kBAt + vb * 2 * kTileBytes, kTileBytes, 1024);
+                    if (leader) {
+                        if (!sh.abort) {
+#pragma unroll
+                            for (int s = 0; s < 4; ++s)
+                                tc::mma_f16_ta(o_at, s_at + 8 * s, v + 128 * s, idesc_o, s > 0 || !begin);
+                        }
+                        tc::mma_commit(tc::smem_addr(&sh.o_half[m]));
+                    }
                     __syncwarp();
-                    if (have)
-                        copy_page(part ? &map_v : &map_k,
-                                  base + (part ? kVAt : kKAt) + st * kTileBytes + lane * B.P * kHd, bar,
-                                  page * B.Hkv + w.h);
-                    issued = 2 * c + part + 1;
-                }
-                page = next;
-            }
-        }
-        // after a wait that gave up: the copies in flight land before the CTA ends
-        for (int i = max(0, issued - 2 * kKs); i < issued && sh.abort; ++i) {
-            const int tile = i / 2, stages = i & 1 ? kVs : kKs;
-            if ((issued - 1 - i) / 2 < stages)
-                tc::mbar_wait_ns(tc::smem_addr(i & 1 ? &sh.v_full[tile % stages] : &sh.k_full[tile % stages]),
-                                 (tile / stages) & 1, lim);
-        }
-    } else if (warp < 3) {
-        // ------------------------------------------------------------ products: warp 1 those of tile A, warp
-        // 2 those of B. A thread's products run in the order of their issue, so S of the next tile may be
-        // issued behind the product that reads P from the same columns.
-        const int m = warp - 1;
-        const bool leader = elect_one();
-        constexpr uint32_t idesc_s = idesc_e4m3(128, 128);
-        constexpr uint32_t idesc_o = tc::idesc_f16(128, 128) | 1u << 7 | 1u << 10 | tc::kIdescTransB;
-        const uint32_t s_at = tmem + m * 128, o_at = tmem + 256 + m * 128;
-        const uint64_t q = tc::sdesc_sw128(base + kQAt + 2 * m * kTileBytes);
-        int k = 0, c = 0, left = take_seg(sh.ring, 0, wait).nt;   // segment, tile, its tiles left: of the next scores
-        bool fresh = true, begin = true;  // whether that tile, and that of the next output, begins its segment
-        auto issue_scores = [&] {         // by one thread
-            const int ks = c % kKs;
-            if (!sh.abort) {
-                const uint64_t kd = tc::sdesc_sw128(base + kKAt + ks * kTileBytes);
+                    wait(sh.p_full[m], j & 1);
+                    tc::fence_after_sync();
+                    if (leader) {
+                        if (!sh.abort) {
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                    for (int s = 0; s < 4; ++s)   // 32 bytes of the rows at a time
-                        mma_e4m3(s_at, q + part * (kTileBytes >> 4) + 2 * s, kd + 2 * s, idesc_s, part + s > 0);
-            }
-            tc::mma_commit(tc::smem_addr(&sh.s_full[m]));
-            tc::mma_commit(tc::smem_addr(&sh.k_free[ks]));
-        };
-#pragma unroll 1
-        for (int j = -1; j < c; ++j) {    // output of tile j, scores of tile j + 1
-            const bool more = left > 0;
-            if (more)
-                wait(sh.k_full[c % kKs], (c / kKs) & 1);
-            if (j >= 0) {
-                const int vb = j % kVb;
-                wait(sh.b_full[vb], (j / kVb) & 1);
-                wait(sh.p_half[m], j & 1);
-                tc::fence_after_sync();
-                // 16 keys at a time: 8 columns of P, 2 KB of V; the first 64 while the others' weights form
-                const uint64_t v = tc::sdesc_sw128_mn(base + kBAt + vb * 2 * kTileBytes, kTileBytes, 1024);
-                if (leader) {
-                    if (!sh.abort) {
-#pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            tc::mma_f16_ta(o_at, s_at + 8 * s, v + 128 * s, idesc_o, s > 0 || !begin);
+                            for (int s = 4; s < 8; ++s)
+                                tc::mma_f16_ta(o_at, s_at + 8 * s, v + 128 * s, idesc_o, 1);
+                        }
+                        if (more && !fresh)
+                            issue_scores();
+                        tc::mma_commit(tc::smem_addr(&sh.o_done[m]));
+                        tc::mma_commit(tc::smem_addr(&sh.b_free[vb]));
                     }
-                    tc::mma_commit(tc::smem_addr(&sh.o_half[m]));
+                    __syncwarp();
                 }
-                __syncwarp();
-                wait(sh.p_full[m], j & 1);
-                tc::fence_after_sync();
-                if (leader) {
-                    if (!sh.abort) {
-#pragma unroll
-                        for (int s = 4; s < 8; ++s)
-                            tc::mma_f16_ta(o_at, s_at + 8 * s, v + 128 * s, idesc_o, 1);
-                    }
-                    if (more && !fresh)
+                if (more && (fresh || j < 0)) {
+                    wait(sh.q_full[m], k & 1);
+                    tc::fence_after_sync();
+                    if (leader)
                         issue_scores();
-                    tc::mma_commit(tc::smem_addr(&sh.o_done[m]));
-                    tc::mma_commit(tc::smem_addr(&sh.b_free[vb]));
+                    __syncwarp();
                 }
-                __syncwarp();
+                begin = fresh;
+                if (more) {
+                    ++c;
+                    fresh = --left == 0;
+                    if (fresh)
+                        left = take_seg(sh.ring, ++k, wait).nt;
+                }
             }
-            if (more && (fresh || j < 0)) {
-                wait(sh.q_full[m], k & 1);
-                tc::fence_after_sync();
-                if (leader)
-                    issue_scores();
-                __syncwarp();
+            if (sh.abort && leader) {   // products in flight end before the tensor memory is freed
+                tc::mma_commit(tc::smem_addr(&sh.drain[m]));
+                tc::mbar_wait_ns(tc::smem_addr(&sh.drain[m]), 0, lim);
             }
-            begin = fresh;
-            if (more) {
-                ++c;
-                fresh = --left == 0;
-                if (fresh)
-                    left = take_seg(sh.ring, ++k, wait).nt;
-            }
+            __syncwarp();
+        } else if (warp == 3) {
+            if (B.n_seq <= kFewSeqs)
+                share = find_share<kRows, kOver, kWhole>(A, sh.share, lane, 32, [] { __syncwarp(); });
+            walk_share<kRows, kOver>(A, share, sh.ring, wait);
+            clear_empty(A, &g_attn_prefill_error);
         }
-        if (sh.abort && leader) {   // products in flight end before the tensor memory is freed
-            tc::mma_commit(tc::smem_addr(&sh.drain[m]));
-            tc::mbar_wait_ns(tc::smem_addr(&sh.drain[m]), 0, lim);
-        }
-        __syncwarp();
-    } else if (warp == 3) {
-        if (B.n_seq <= kFewSeqs)
-            share = find_share<kRows, kOver, kWhole>(A, sh.share, lane, 32, [] { __syncwarp(); });
-        walk_share<kRows, kOver>(A, share, sh.ring, wait);
-        clear_empty(A, &g_attn_prefill_error);
     } else if (warp < 12) {
         // ------------------------------------------------------------ scores to weights: a row per thread
+        registers_up<160>();
         const int m = (warp - 4) >> 2, row = (tid - 128) & 127, x = m * 128 + row;
         const uint32_t lane_at = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + m * 128 + lane_at, o_at = tmem + 256 + m * 128 + lane_at;
@@ -761,6 +778,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
         }
     } else {
         // ------------------------------------------------------------ V to bf16: a key per thread
+        registers_down<96>();
         const int t128 = tid - 384;
         int c = 0;
 #pragma unroll 1
@@ -799,36 +817,28 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                 wait(sh.v_full[vst], (c / kVs) & 1);
                 const uint8_t *src = mem + kVAt + vst * kTileBytes + t128 * kHd;
                 uint8_t *dst = mem + kBAt + vb * 2 * kTileBytes + (t128 >> 3) * 1024 + (t128 & 7) * 128;
-                // four 16-byte pieces in flight at a time: one warp per scheduler does this, so its own
-                // independent work is all that hides its latencies
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    uint4 raw[4];
+#pragma unroll 2
+                for (int i = 0; i < 8; ++i) {
+                    const uint4 raw = dead ? make_uint4(0, 0, 0, 0)
+                                           : *reinterpret_cast<const uint4 *>(src + ((i ^ (t128 & 7)) << 4));
+                    const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+                    uint32_t o[8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        raw[i] = *reinterpret_cast<const uint4 *>(src + (((4 * half + i) ^ (t128 & 7)) << 4));
-                    uint8_t *const to = dst + half * kTileBytes;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t in[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-                        uint32_t o[8];
-#pragma unroll
-                        for (int z = 0; z < 4; ++z) {
-                            const uint32_t code = dead ? 0u : in[z];
-                            o[2 * z] = mul_bf16x2(codes_bf16(__byte_perm(code, 0, 0x1404)), f1);
-                            o[2 * z + 1] = mul_bf16x2(codes_bf16(__byte_perm(code, 0, 0x3424)), f1);
-                        }
-                        if (e2 != 0) {
-#pragma unroll
-                            for (int z = 0; z < 8; ++z)
-                                o[z] = mul_bf16x2(o[z], f2);
-                        }
-                        // dimensions 16 (4 half + i) ..: two 16-byte pieces
-                        *reinterpret_cast<uint4 *>(to + (((2 * i) ^ (t128 & 7)) << 4)) =
-                            make_uint4(o[0], o[1], o[2], o[3]);
-                        *reinterpret_cast<uint4 *>(to + (((2 * i + 1) ^ (t128 & 7)) << 4)) =
-                            make_uint4(o[4], o[5], o[6], o[7]);
+                    for (int z = 0; z < 4; ++z) {
+                        o[2 * z] = mul_bf16x2(codes_bf16(__byte_perm(in[z], 0, 0x1404)), f1);
+                        o[2 * z + 1] = mul_bf16x2(codes_bf16(__byte_perm(in[z], 0, 0x3424)), f1);
                     }
+                    if (e2 != 0) {
+#pragma unroll
+                        for (int z = 0; z < 8; ++z)
+                            o[z] = mul_bf16x2(o[z], f2);
+                    }
+                    // dimensions 16 i .. 16 i + 15: two 16-byte pieces of half i / 4
+                    uint8_t *half = dst + (i >> 2) * kTileBytes;
+                    const int p0 = (2 * i) & 7;
+                    *reinterpret_cast<uint4 *>(half + ((p0 ^ (t128 & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4 *>(half + (((p0 + 1) ^ (t128 & 7)) << 4)) =
+                        make_uint4(o[4], o[5], o[6], o[7]);
                 }
                 arrive(sh.v_free[vst]);
                 tc::fence_smem_to_async();
