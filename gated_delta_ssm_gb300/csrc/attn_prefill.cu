@@ -38,7 +38,7 @@ constexpr int kThreads = 512;
 constexpr int kRows = 256;                    // q rows per block
 constexpr int kOver = 6;                      // what a block costs besides its tiles, in tiles
 constexpr int kWhole = 8;                     // most tiles of blocks that are not worth splitting
-constexpr int kKs = 3, kVs = 2, kVb = 2;      // stages: K codes, V codes, V in bf16
+constexpr int kKs = 2, kVs = 2, kVb = 2;      // stages: K codes, V codes, V in bf16
 constexpr uint32_t kQAt = 0;                  // [A, B][hi, lo] 128 rows of 128 bytes
 constexpr uint32_t kKAt = kQAt + 4 * kTileBytes;
 constexpr uint32_t kVAt = kKAt + kKs * kTileBytes;
@@ -817,7 +817,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                 wait(sh.v_full[vst], (c / kVs) & 1);
                 const uint8_t *src = mem + kVAt + vst * kTileBytes + t128 * kHd;
                 uint8_t *dst = mem + kBAt + vb * 2 * kTileBytes + (t128 >> 3) * 1024 + (t128 & 7) * 128;
-#pragma unroll 2
+#pragma unroll 1   // two or four pieces in flight are slower (865 against 896 and 930 us): their code crowds the others out
                 for (int i = 0; i < 8; ++i) {
                     const uint4 raw = dead ? make_uint4(0, 0, 0, 0)
                                            : *reinterpret_cast<const uint4 *>(src + ((i ^ (t128 & 7)) << 4));
