@@ -588,7 +588,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                         left = take_seg(sh.ring, ++k, wait).nt;
                 }
             }
-            if (sh.abort && leader) {   // products in flight end before the tensor memory is freed
+            if (leader) {   // every product, and every arrival that a commit still owes, ends before the CTA does
                 tc::mma_commit(tc::smem_addr(&sh.drain[m]));
                 tc::mbar_wait_ns(tc::smem_addr(&sh.drain[m]), 0, lim);
             }
