@@ -300,6 +300,7 @@ gdn_status attention(const void *q, int64_t q_stride, const gdn_kv_cache *cache,
     a.window = window;
     a.ws = static_cast<uint8_t *>(workspace);
     a.wait_ns = gdn::kDefaultWaitNs;
+    a.first_wait_ns = gdn::first_wait_override_ns();
     return from_cuda(prefill ? gdn::attn::launch_prefill(a, as_cuda(stream))
                              : gdn::attn::launch_decode(a, as_cuda(stream)));
 }

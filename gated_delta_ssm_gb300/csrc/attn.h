@@ -44,7 +44,7 @@ struct AttnArgs {
     int window;
     uint8_t *ws;
     int sm_count;
-    uint64_t wait_ns;
+    uint64_t wait_ns, first_wait_ns;   // limits of the bounded waits, and of a CTA's first
 };
 
 cudaError_t launch_append(const AppendArgs &a, bool bf16, cudaStream_t s);

@@ -216,6 +216,13 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
         wait1(bar, parity);
         __syncwarp();
     };
+    auto wait_first = [&](const uint64_t &bar, uint32_t parity) {   // the CTA's first, whose limit a test sets
+        if (!wait_phase(tc::smem_addr(&bar), parity, A.first_wait_ns, &sh.abort)) {
+            sh.abort = 1;
+            failed = true;
+        }
+        __syncwarp();
+    };
     auto arrive = [&](const uint64_t &bar) { tc::mbar_arrive(tc::smem_addr(&bar)); };
 
     if (warp == 0) {
@@ -224,7 +231,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
         const int per_tile = kTile >> page_shift;
 #pragma unroll 1
         for (int k = 0;; ++k) {
-            const Seg w = take_seg(sh.ring, k, wait);
+            const Seg w = take_seg(sh.ring, k, wait, &sh.abort);
             if (w.nt == 0)
                 break;
             const int32_t *table = B.page_table + (int64_t)w.b * B.max_pages;
@@ -272,7 +279,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
         const bool leader = elect_one();
         constexpr uint32_t idesc_s = idesc_e4m3(128, NR);
         constexpr uint32_t idesc_o = idesc_e4m3(128, NR) | kIdescTransA;
-        int k = 0, c = 0, left = take_seg(sh.ring, 0, wait).nt;   // segment, tile, its tiles left: of the next scores
+        int k = 0, c = 0, left = take_seg(sh.ring, 0, wait, &sh.abort).nt;   // segment, tile, its tiles left: of the next scores
 #pragma unroll 1
         for (int j = -2; j < c; ++j) {      // scores of tile j + 2 behind the output of tile j
             if (j >= 0) {
@@ -301,7 +308,10 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
             if (left > 0) {
                 const int item = 2 * c, st = item % C::kItems;
                 wait(sh.q_full[k & 1], (k >> 1) & 1);
-                wait(sh.full[st], (item / C::kItems) & 1);
+                if (c == 0)
+                    wait_first(sh.full[st], 0);
+                else
+                    wait(sh.full[st], (item / C::kItems) & 1);
                 tc::fence_after_sync();
                 if (leader) {
                     if (!sh.abort) {
@@ -322,7 +332,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
                 __syncwarp();
                 ++c;
                 if (--left == 0)
-                    left = take_seg(sh.ring, ++k, wait).nt;
+                    left = take_seg(sh.ring, ++k, wait, &sh.abort).nt;
             }
         }
         if (leader) {   // every product, and every arrival that a commit still owes, ends before the CTA does
@@ -335,7 +345,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
         const int u = lane & 7, r4 = lane >> 3;
 #pragma unroll 1
         for (int k = 0;; ++k) {
-            const Seg w = take_seg(sh.ring, k, wait);
+            const Seg w = take_seg(sh.ring, k, wait, &sh.abort);
             if (w.nt == 0)
                 break;
             const int par = k & 1;
@@ -371,7 +381,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
     } else if (warp == 3) {
         if (B.n_seq <= kFewSeqs)
             share = find_share<kMaxDecodeRows, kOver, kWhole>(A, sh.share, lane, 32, [] { __syncwarp(); });
-        walk_share<kMaxDecodeRows, kOver>(A, share, sh.ring, wait);
+        walk_share<kMaxDecodeRows, kOver>(A, share, sh.ring, wait, &sh.abort);
         clear_empty(A, &g_attn_decode_error);
     } else if (warp < 4 + 4 * C::kWgs) {
         // ------------------------------------------------------------ scores to weights: a key per thread
@@ -383,7 +393,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
         int i = 0;
 #pragma unroll 1
         for (int k = 0;; ++k) {
-            const Seg w = take_seg(sh.ring, k, wait);
+            const Seg w = take_seg(sh.ring, k, wait, &sh.abort);
             if (w.nt == 0)
                 break;
             const int par_q = k & 1;
@@ -537,8 +547,8 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
         int i = 0;
 #pragma unroll 1
         for (int k = 0;; ++k) {
-            const Seg w = take_seg(sh.ring, k, wait);
-            if (w.nt == 0)
+            const Seg w = take_seg(sh.ring, k, wait, &sh.abort);
+            if (named_any(1, 128, w.nt == 0))   // the four warps meet at barriers, so they end together
                 break;
             const int par_q = k & 1;
             float o[NR];               // O of row r is o 2^o_ref[r]

@@ -453,6 +453,13 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
         }
         __syncwarp();
     };
+    auto wait_first = [&](const uint64_t &bar, uint32_t parity) {   // the CTA's first, whose limit a test sets
+        if (!wait_phase(tc::smem_addr(&bar), parity, A.first_wait_ns, &sh.abort)) {
+            sh.abort = 1;
+            failed = true;
+        }
+        __syncwarp();
+    };
     auto arrive = [&](const uint64_t &bar) { tc::mbar_arrive(tc::smem_addr(&bar)); };
 
     // Registers move to the two groups of warps that hold rows: 128 (88 + 160 + 160 + 96) of the 65,536 that the
@@ -465,7 +472,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
             const int per_tile = kTile >> page_shift;
 #pragma unroll 1
             for (int k = 0;; ++k) {
-                const Seg w = take_seg(sh.ring, k, wait);
+                const Seg w = take_seg(sh.ring, k, wait, &sh.abort);
                 if (w.nt == 0)
                     break;
                 const int32_t *table = B.page_table + (int64_t)w.b * B.max_pages;
@@ -522,7 +529,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
             constexpr uint32_t idesc_o = tc::idesc_f16(128, 128) | 1u << 7 | 1u << 10 | tc::kIdescTransB;
             const uint32_t s_at = tmem + m * 128, o_at = tmem + 256 + m * 128;
             const uint64_t q = tc::sdesc_sw128(base + kQAt + 2 * m * kTileBytes);
-            int k = 0, c = 0, left = take_seg(sh.ring, 0, wait).nt;   // segment, tile, its tiles left: of the next scores
+            int k = 0, c = 0, left = take_seg(sh.ring, 0, wait, &sh.abort).nt;   // segment, tile, its tiles left: of the next scores
             bool fresh = true, begin = true;  // whether that tile, and that of the next output, begins its segment
             auto issue_scores = [&] {         // by one thread
                 const int ks = c % kKs;
@@ -540,7 +547,9 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
 #pragma unroll 1
             for (int j = -1; j < c; ++j) {    // output of tile j, scores of tile j + 1
                 const bool more = left > 0;
-                if (more)
+                if (more && c == 0)
+                    wait_first(sh.k_full[0], 0);
+                else if (more)
                     wait(sh.k_full[c % kKs], (c / kKs) & 1);
                 if (j >= 0) {
                     const int vb = j % kVb;
@@ -585,7 +594,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                     ++c;
                     fresh = --left == 0;
                     if (fresh)
-                        left = take_seg(sh.ring, ++k, wait).nt;
+                        left = take_seg(sh.ring, ++k, wait, &sh.abort).nt;
                 }
             }
             if (leader) {   // every product, and every arrival that a commit still owes, ends before the CTA does
@@ -596,7 +605,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
         } else if (warp == 3) {
             if (B.n_seq <= kFewSeqs)
                 share = find_share<kRows, kOver, kWhole>(A, sh.share, lane, 32, [] { __syncwarp(); });
-            walk_share<kRows, kOver>(A, share, sh.ring, wait);
+            walk_share<kRows, kOver>(A, share, sh.ring, wait, &sh.abort);
             clear_empty(A, &g_attn_prefill_error);
         }
     } else if (warp < 12) {
@@ -614,7 +623,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
         float ref = 0.0f, l = 0.0f;
 #pragma unroll 1
         for (int k = 0;; ++k) {
-            const Seg nx = take_seg(sh.ring, k, wait);
+            const Seg nx = take_seg(sh.ring, k, wait, &sh.abort);
             if (nx.nt > 0) {
                 // The next segment's q rows, 32 by each warp, while the last segment's last product runs (the
                 // products that read that segment's q are done: its scores were here). A row's bf16 pieces
@@ -783,7 +792,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
         int c = 0;
 #pragma unroll 1
         for (int k = 0;; ++k) {
-            const Seg w = take_seg(sh.ring, k, wait);
+            const Seg w = take_seg(sh.ring, k, wait, &sh.abort);
             if (w.nt == 0)
                 break;
             const int32_t *table = B.page_table + (int64_t)w.b * B.max_pages;

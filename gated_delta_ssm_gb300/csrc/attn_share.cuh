@@ -212,9 +212,11 @@ __device__ __forceinline__ Share find_share(const AttnArgs &A, ShareShared<THREA
     return r;
 }
 
-// One warp walks the share and fills the ring; `wait` is the kernel's bounded wait.
+// One warp walks the share and fills the ring; `wait` is the kernel's bounded wait, *abort what it leaves when it
+// gives up.
 template <int ROWS, int OVER, typename W>
-__device__ __forceinline__ void walk_share(const AttnArgs &A, const Share &r, Ring &ring, W wait)
+__device__ __forceinline__ void walk_share(const AttnArgs &A, const Share &r, Ring &ring, W wait,
+                                           const volatile int *abort)
 {
     const Batch &B = A.b;
     const int lane = threadIdx.x & 31;
@@ -297,6 +299,8 @@ __device__ __forceinline__ void walk_share(const AttnArgs &A, const Share &r, Ri
         const int slot = k % kRing;
         if (k >= kRing)
             wait(ring.free[slot], (k / kRing - 1) & 1);
+        if (__any_sync(0xffffffffu, *abort != 0))
+            return;
         if (lane == 0) {
             ring.seg[slot] = q;
             tc::mbar_arrive(tc::smem_addr(&ring.full[slot]));
@@ -307,14 +311,16 @@ __device__ __forceinline__ void walk_share(const AttnArgs &A, const Share &r, Ri
     }
 }
 
-// Segment k of the ring, for a whole warp; its slot is handed back at once.
+// Segment k of the ring, for a whole warp; its slot is handed back at once. After a wait that gave up there are
+// no more segments: the walk has stopped, and what the slot holds is an old one.
 template <typename W>
-__device__ __forceinline__ Seg take_seg(Ring &ring, int k, W wait)
+__device__ __forceinline__ Seg take_seg(Ring &ring, int k, W wait, const volatile int *abort)
 {
     const int slot = k % kRing;
     wait(ring.full[slot], (k / kRing) & 1);
-    const Seg q = ring.seg[slot];
-    __syncwarp();
+    Seg q = ring.seg[slot];
+    if (__any_sync(0xffffffffu, *abort != 0))
+        q.nt = 0;
     if ((threadIdx.x & 31) == 0)
         tc::mbar_arrive(tc::smem_addr(&ring.free[slot]));
     return q;

@@ -14,8 +14,9 @@ extern "C" {
 
 /*
  * Limit, in nanoseconds of the GPU's global timer, of the first bounded wait
- * of the prefill's sequential pass and of each CTA's first tile-copy wait in
- * the multi-token conv, for every later call in this process (0 restores the
+ * of the prefill's sequential pass, of each CTA's first tile-copy wait in
+ * the multi-token conv and of each CTA's first wait for keys in
+ * gdn_attn_decode and gdn_attn_prefill, for every later call in this process (0 restores the
  * default of 2 s). A tiny value makes those waits give up while the work they
  * wait for is still in flight, so a test can check that the kernels then set
  * their bit of the device error word (gdn_check_device), drain what they
