@@ -103,14 +103,15 @@ __device__ __forceinline__ float redux_max(float x)
     return y;
 }
 
-// Two e4m3 numbers whose sum is (x, y) to within 2^-8 of each, down to steps of 2^-9: the low byte of
-// each result is x's.
+// Two e4m3 numbers whose sum is (x, y), each below 2^15, to within 2^-8 of each and 2^-10: the low byte of each
+// result is x's. By way of fp16, which both conversions and the difference between them take two at a time; its
+// rounding, 2^-11, is an eighth of the sum's.
 __device__ __forceinline__ void split_e4m3(float x, float y, uint32_t &hi, uint32_t &lo)
 {
-    hi = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
-    const float2 back =
-        __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3)));
-    lo = __nv_cvt_float2_to_fp8x2(make_float2(x - back.x, y - back.y), __NV_SATFINITE, __NV_E4M3);
+    const __half2 v = __floats2half2_rn(x, y);
+    hi = __nv_cvt_halfraw2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+    const __half2 back(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3));
+    lo = __nv_cvt_halfraw2_to_fp8x2(__hsub2(v, back), __NV_SATFINITE, __NV_E4M3);
 }
 
 // 16 bf16 elements as floats.
