@@ -233,6 +233,13 @@ __device__ __forceinline__ void row_weights(uint32_t s_at, const RowMask &mask_o
     }
 }
 
+// 8 columns of this thread's lane.
+__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&v)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]));
+}
+
 // Weights of a row whose scores are capped at no more than kMostCap: the weights themselves stay within the
 // range of the numbers that hold them, so no reference is needed, and no maximum. In base 2 the capped score is
 // c - 2 c / (1 + e^(2 s / cap)); its absolute error, c 2^-22, is far below a bf16 weight's rounding. One
@@ -244,39 +251,34 @@ __device__ __forceinline__ float half_weights_capped(uint32_t s_at, int half_til
     uint64_t sum[2] = {0, 0};
     const uint64_t one = pack2(1.0f, 1.0f), c2 = pack2(c, c), m2c = pack2(-2.0f * c, -2.0f * c);
     const float f = 2.0f * kLog2e / c;    // factor() gives base-2 scores: 2 log2 e s / cap = (2 log2 e / c) (s log2 e)
-#pragma unroll 1
-    for (int q4 = 2 * half_tile; q4 < 2 * half_tile + 2; ++q4) {
-        uint32_t v[32], y[16];
-        tmem_get32(s_at + 32 * q4, v);
-        tmem_wait32(v);
-        const uint32_t mask = WHOLE ? 0xffffffffu : mask_of(q4);
+#pragma unroll 2
+    for (int x = 4 * half_tile; x < 4 * half_tile + 4; ++x) {   // 16 columns at a time
+        uint32_t v[16], y[8];
+        tmem_get16(s_at + 16 * x, v);
+        tmem_wait16(v);
+        const uint32_t mask = WHOLE ? 0xffffu : mask_of(x / 2) >> (16 * (x & 1));
+        const float fk = factor(x) * f;
+        const uint64_t fk2 = pack2(fk, fk);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const float fk = factor(2 * q4 + half) * f;
-            const uint64_t fk2 = pack2(fk, fk);
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-                const int i = 16 * half + e;
-                float2 a = make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-                if (!WHOLE) {   // columns that are not seen may hold NaN, and pairs share a reciprocal
-                    a.x = mask >> i & 1 ? a.x : 0.0f;
-                    a.y = mask >> (i + 1) & 1 ? a.y : 0.0f;
-                }
-                a = unpack2(mul2(pack2(a.x, a.y), fk2));
-                a = unpack2(add2(pack2(ex2(fminf(a.x, 60.0f)), ex2(fminf(a.y, 60.0f))), one));
-                const float r = rcp(a.x * a.y);
-                const float2 w = unpack2(fma2(mul2(pack2(r, r), pack2(a.y, a.x)), m2c, c2));
-                float2 z = make_float2(ex2(w.x), ex2(w.y));
-                if (!WHOLE) {
-                    z.x = mask >> i & 1 ? z.x : 0.0f;
-                    z.y = mask >> (i + 1) & 1 ? z.y : 0.0f;
-                }
-                const uint64_t z2 = pack2(z.x, z.y);
-                sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], z2);
-                y[8 * half + e / 2] = pack_bf16x2(z.x, z.y);
+        for (int i = 0; i < 16; i += 2) {
+            float2 a = make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+            if (!WHOLE) {   // columns that are not seen may hold NaN, and pairs share a reciprocal
+                a.x = mask >> i & 1 ? a.x : 0.0f;
+                a.y = mask >> (i + 1) & 1 ? a.y : 0.0f;
             }
+            a = unpack2(mul2(pack2(a.x, a.y), fk2));
+            a = unpack2(add2(pack2(ex2(fminf(a.x, 60.0f)), ex2(fminf(a.y, 60.0f))), one));
+            const float r = rcp(a.x * a.y);
+            const float2 w = unpack2(fma2(mul2(pack2(r, r), pack2(a.y, a.x)), m2c, c2));
+            float2 z = make_float2(ex2(w.x), ex2(w.y));
+            if (!WHOLE) {
+                z.x = mask >> i & 1 ? z.x : 0.0f;
+                z.y = mask >> (i + 1) & 1 ? z.y : 0.0f;
+            }
+            sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pack2(z.x, z.y));
+            y[i / 2] = pack_bf16x2(z.x, z.y);
         }
-        tc::tmem_st16u(s_at + 16 * q4, y);
+        tmem_st8u(s_at + 8 * x, y);
     }
     const float2 t = unpack2(add2(sum[0], sum[1]));
     return t.x + t.y;
