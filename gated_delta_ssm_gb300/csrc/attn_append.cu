@@ -127,6 +127,67 @@ __device__ __forceinline__ void rotate_row(Row16 &r, const AppendArgs &A, int u,
     }
 }
 
+// a*c - b*s rounded to odd: to the neighbour in 32 bits whose last bit is set, unless it is exact. Rounding that to
+// e4m3 rounds the exact value, and a value just above 448 s stays above it; rounded to nearest, a value within 2^-25
+// of itself of such a border would be taken to lie on it. The products are split into two numbers each and added
+// with their errors. `near` is what to keep where a sum is not finite.
+__device__ __forceinline__ float turn_to_odd(float a, float c, float b, float s, float near)
+{
+    const float p = __fmul_rn(a, c), pe = __fmaf_rn(a, c, -p), w = __fmul_rn(b, s), we = __fmaf_rn(b, s, -w);
+    const float h = __fsub_rn(p, w), z = __fsub_rn(h, p);
+    const float t = __fsub_rn(__fsub_rn(p, __fsub_rn(h, z)), __fadd_rn(w, z));
+    const float l = __fadd_rn(t, __fsub_rn(pe, we));
+    const float x = __fadd_rn(h, l), r = __fsub_rn(l, __fsub_rn(x, h));   // the exact value is x + r
+    if (!(fabsf(r) > 0.0f))
+        return r == r ? x : near;
+    const int bits = __float_as_int(x);
+    return bits & 1 ? x : __int_as_float((bits ^ __float_as_int(r)) < 0 ? bits - 1 : bits + 1);
+}
+
+// Whether a value's last 19 bits are within 2 of zero, as they are beside every border of e4m3 times a power of two:
+// midpoints have four bits behind the leading one at most, 448 two, and rotate_pair is within about a unit.
+__device__ __forceinline__ bool beside_border(const Row16 &x)
+{
+    uint32_t m = ~0u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        m = min(m, min((__float_as_uint(x.a[e]) + 2) & 0x7ffffu, (__float_as_uint(x.b[e]) + 2) & 0x7ffffu));
+    return m <= 4;
+}
+
+__device__ __forceinline__ float load_again(const float *p) { return *const_cast<const volatile float *>(p); }
+__device__ __forceinline__ float load_again(const __nv_bfloat16 *p)
+{
+    return __uint_as_float((uint32_t)*reinterpret_cast<const volatile unsigned short *>(p) << 16);
+}
+
+// rotate_row of this thread's pieces of `row`, rounded to odd; y holds rotate_row's result. Few rows come here, so
+// inputs and angles are loaded again, one pair at a time, and cost the others no registers.
+template <typename T>
+__device__ __forceinline__ void rotate_row_to_odd(Row16 &y, const T *row, const AppendArgs &A, int u, int pos)
+{
+    const int64_t at = (int64_t)pos * (A.rot / 2) + u * 8;
+    int ca, cb;
+    pieces(u, A.rot, A.interleaved, ca, cb);
+    auto pair = [&](float &ya, float &yb, int ia, int ib, int i) {
+        const float a = load_again(row + ia), b = load_again(row + ib);
+        const float c = load_again(A.cos + at + i), s = load_again(A.sin + at + i);
+        ya = turn_to_odd(a, c, b, s, ya);
+        yb = turn_to_odd(b, c, -a, s, yb);
+    };
+    if (A.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            pair(y.a[2 * i], y.a[2 * i + 1], ca + 2 * i, ca + 2 * i + 1, i);
+            pair(y.b[2 * i], y.b[2 * i + 1], cb + 2 * i, cb + 2 * i + 1, 4 + i);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            pair(y.a[i], y.b[i], ca + i, cb + i, i);
+    }
+}
+
 // The smallest power of two s with amax <= 448 s (448 = 0.875 * 2^9), at least 2^-100.
 __device__ __forceinline__ float pow2_scale(float amax)
 {
@@ -278,6 +339,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) append_kernel(const __grid_cons
                 Angles t;
                 load_angles(t, A, u, pos);
                 rotate_row(x[i], A, u, t);
+                if (u * 16 < A.rot && beside_border(x[i]))   // one row in some thousands
+                    rotate_row_to_odd(x[i], src + (int64_t)(first_row + pos) * stride + h * kHd, A, u, pos);
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
