@@ -541,7 +541,7 @@ def _load_torch():
         _BF16_DT, _ACT_DT, _I32_DT = (torch.bfloat16,), (torch.float32, torch.bfloat16), (torch.int32,)
         if torch.cuda.is_available():
             _current_device = torch.cuda.current_device
-            # the current stream's handle without building a Stream object (3 us on the Arm host)
+            # the current stream's handle without building a Stream object, which takes 3 us
             _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                                   lambda dev: torch.cuda.current_stream(dev).cuda_stream)
         _torch = torch

@@ -15,6 +15,14 @@
 //                 unrotated elements rot + (u - rot/16)*16 ..;
 //   interleaved   elements u*16 .. u*16 + 15.
 // Either way thread u's angles are u*8 .. u*8 + 7 of the position's table row.
+//
+// A key's code is that of its exact rotation: the few values that 32 bits put on a rounding border are turned again
+// and rounded to odd. The rotation of q is within about a unit of 32 bits before its one rounding to bf16.
+//
+// Measured: 4 x 8192 tokens, 16 q heads on 4, bf16: 74 us, 5.2 TB/s of the bytes it cannot do without. Its warps
+// wait for loads (5.6 of 12 cycles an issue); 64 registers, four CTAs of 256 threads an SM, measured best (three
+// CTAs: 76.7 us; 512 threads: 83 us; before the angles were shared by a token's heads: 102 us). A single token: the
+// call's 8 us on the host.
 #include <cuda_fp8.h>
 
 #include "attn_device.cuh"

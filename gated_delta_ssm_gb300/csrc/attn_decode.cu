@@ -23,6 +23,13 @@
 // shared out equally over the CTAs (attn_share.cuh); a (sequence, head) that
 // spans CTAs leaves 32-bit partial results which a second kernel joins.
 //
+// Measured: 64 sequences of 800 to 8191 tokens, 32 q heads on 8, one token each:
+// 102 us, 5.6 TB/s (DRAM busy 71% of the time, the tensor pipe 8%). One sequence
+// of 131071 tokens, 4 KV heads: 42 us, of which about 8 pass before the first
+// tile is used and 5 in the join. 32 drafts of four tokens, cap 30, R = 32: 63 us,
+// bound by instructions (about 8200 warp instructions a tile); four groups of
+// softmax warps there take 70 us, two columns' loops unrolled 73 us.
+//
 // Roles of a CTA: warp 0 copies pages to shared memory, warp 1 issues the
 // products, warp 2 splits the q rows of the next segment, warp 3 walks the share,
 // one or two groups of four warps hold a key per thread and turn scores into

@@ -1,5 +1,7 @@
 // attn_join.cu -- joins the partial results of the attention kernels: a block of
-// q rows whose keys were shared out over several CTAs.
+// q rows whose keys were shared out over several CTAs. Bound by latency: about
+// 5 us behind a decode of one long sequence.
+
 #include "attn_device.cuh"
 #include "cluster.cuh"
 #include "gdn_device.cuh"

@@ -19,6 +19,14 @@
 // equal contiguous shares, and q blocks that span shares are joined by a second
 // kernel, so causal and ragged blocks of any number fill the GPU.
 //
+// Measured: 4 x 8192 tokens, 16 q heads on 4: 861 us, 1.28 PFLOP/s. The products
+// of a pair of tiles take 2051 cycles back to back; with the other roles' shared
+// memory traffic and the chain scores, weights, output they take 2800 to 3000.
+// 1024 tokens behind 32768, 32 heads on 4, cap 50: 622 us, bound by three
+// exponentials and a half reciprocal a score. Window 1000, 6 prompts: 84 us, where
+// about 12000 cycles a block for q and the output count for as much as its tiles.
+// Loops are short on purpose: unrolled further, fetching instructions stalls them.
+//
 // Roles of a CTA (512 threads): warp 0 copies pages, warps 1 and 2 issue the
 // products of tiles A and B, warp 3 walks the share (attn_share.cuh), warps 4-7
 // and 8-11 split q and hold a row each of tiles A and B, warps 12-15 convert V.

@@ -22,6 +22,8 @@
  *               accepted counts) is read after it, in stream order. (A
  *               launch of at most one wave also asks for its state rows to
  *               be brought into L2 before then, which reads nothing.)
+ *               gdn_attn_append, gdn_attn_decode and gdn_attn_prefill launch
+ *               in the same way and read every argument after it.
  *   Errors      Host-side validation runs before anything is launched. A
  *               call that returns anything but GDN_OK has enqueued nothing,
  *               except GDN_ERR_CUDA, where the launch itself failed;
@@ -31,8 +33,10 @@
  *               bits (see gdn_check_device): calls from several host threads
  *               and streams are safe as long as their buffers do not overlap.
  *   Precision   Parameters, recurrent state, conv history and all outputs are
- *               float32 (gdn_decode_step_bf16_state excepted); activations are
- *               float32 or bf16 (gdn_dtype). All arithmetic is float32.
+ *               float32 (gdn_decode_step_bf16_state and the attention calls
+ *               excepted); activations are float32 or bf16 (gdn_dtype). All
+ *               arithmetic is float32 but for the tensor-core products of the
+ *               prefill and attention calls, whose sums are float32.
  *
  * SHAPES (gdn_dims)
  *   B   = n_seq, Hq = n_qk_heads, Hv = n_v_heads (a multiple of Hq; r = Hv/Hq),
@@ -462,7 +466,7 @@ gdn_status gdn_prefill_chunked_noalloc(float *state, float *conv_state, const vo
  *   have raised.
  *
  * SUPPORTED  head_dim 128; page_size 16, 32, 64 or 128; Hq a multiple of Hkv,
- *   G = Hq / Hkv at most 16.
+ *   G = Hq / Hkv at most 16; n_tokens * G at most 2^27 - 256.
  */
 typedef struct gdn_attn_dims {
     int32_t n_seq;        /* >= 1, <= 65535 */
@@ -525,7 +529,8 @@ gdn_status gdn_attn_append(const void *q, int64_t q_stride, const void *k, int64
 
 /*
  * Workspace bytes of gdn_attn_decode (prefill = 0) or gdn_attn_prefill
- * (prefill = 1); it depends on the heads and on max_q, not on the lengths.
+ * (prefill = 1); it depends on the heads, on max_q and on the current device's
+ * number of SMs, not on the lengths, n_seq or n_tokens.
  * Returns 0 for invalid or unsupported dims.
  */
 size_t gdn_attn_workspace_bytes(const gdn_attn_dims *dims, int32_t prefill);
@@ -543,10 +548,15 @@ size_t gdn_attn_workspace_bytes(const gdn_attn_dims *dims, int32_t prefill);
  *   workspace  device scratch of gdn_attn_workspace_bytes(dims, 0) bytes,
  *        16-byte aligned; contents on entry do not matter. Calls that overlap
  *        on the GPU need separate workspaces.
- * Scores, statistics and sums are float32.
+ * Scores, statistics and sums are float32. Keys and values enter the products
+ * as they are held. q enters as two e4m3 numbers, exact down to 2^-18 of the
+ * row's largest element; a weight is rounded to 2^-8 of itself (two e4m3
+ * numbers, bf16 in gdn_attn_prefill) before it meets v, not in the sum.
+ * Two launches: the second joins rows whose keys were shared out.
  * Errors: INVALID_ARG (null, sizes, alignment, scale or softcap not finite,
  * softcap or window negative, workspace too small), UNSUPPORTED (head_dim,
- * page_size, G, G * max_q > 64).
+ * page_size, G, n_tokens * G, G * max_q > 64), CUDA (besides a failed launch:
+ * a batch of more than 2e9 pairs of row block and 128-key tile).
  */
 gdn_status gdn_attn_decode(const void *q, int64_t q_stride, const gdn_kv_cache *cache,
                            const int32_t *q_start, const int32_t *kv_len, void *out,
@@ -587,8 +597,8 @@ gdn_status gdn_attn_prefill(const void *q, int64_t q_stride, const gdn_kv_cache 
  *   bit 512 gdn_attn_append met a key or value that is not finite
  *   bit 1024 an attention kernel gave up a wait (its outputs are not valid)
  * The one wait not bounded by the library is the hardware's tensor-memory
- * allocation at the start of the prefill kernels, which lasts until CTAs of
- * other launches on the same SM release their columns. This call waits for
+ * allocation at the start of the prefill and attention kernels, which lasts
+ * until CTAs of other launches on the same SM release their columns. This call waits for
  * all work on the device (it synchronises), reads the word into *code (may be
  * NULL) and clears it. Returns GDN_OK when no bit was set, GDN_ERR_DEVICE when
  * one was, GDN_ERR_CUDA if the read failed.
