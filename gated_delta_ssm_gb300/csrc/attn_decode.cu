@@ -49,7 +49,6 @@ namespace {
 
 constexpr int kOver = 1;     // what a block costs besides its tiles, in tiles
 constexpr int kWhole = 3;    // most tiles of blocks that are not worth splitting
-constexpr float kNoRef = -1e30f;   // below every reference, and finite: 2^(-inf - kNoRef) is 0
 
 template <int NR>            // rows, padded
 struct Cfg {

@@ -41,6 +41,9 @@ struct PartMeta {
     int owner, pad[3];
 };
 constexpr int kPartRow = kHd + 4;   // 128 sums, l, m, two unused
+// The reference m of a row that a part sees no key of: below every other, so that the join goes by the parts that
+// hold the row's keys, however low their scores lie; and finite: 2^(-inf - kNoRef) is 0.
+constexpr float kNoRef = -1e30f;
 
 __device__ __forceinline__ float *part_slots(uint8_t *ws, unsigned grid)
 {

@@ -714,7 +714,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                     }
                 }
                 if (joined) {
-                    *reinterpret_cast<float2 *>(part + kHd) = make_float2(l, ref);
+                    *reinterpret_cast<float2 *>(part + kHd) = make_float2(l, l == 0.0f ? kNoRef : ref);   // NaN keeps ref
                     if (w.begins && x == 0)
                         meta[blockIdx.x] = {w.b, w.h, w.blk, w.last_cta, 1, {}};
                 }
