@@ -461,8 +461,8 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
 #pragma unroll
                         for (int r = 0; r < 8; r += 2) {
                             const float2 y = unpack2(mul2(pack2(x[r], x[r + 1]), mul2(f2[r / 2], ks2)));
-                            const float a = 1.0f + ex2(fminf(y.x * cap_in, 60.0f));
-                            const float b = 1.0f + ex2(fminf(y.y * cap_in, 60.0f));
+                            const float a = 1.0f + ex2(min_nan(y.x * cap_in, 60.0f));
+                            const float b = 1.0f + ex2(min_nan(y.y * cap_in, 60.0f));
                             x[r] = fmaf(rcp(a), -2.0f * cap2, cap2 + ev);
                             x[r + 1] = fmaf(rcp(b), -2.0f * cap2, cap2 + ev);
                         }

@@ -275,7 +275,7 @@ __device__ __forceinline__ float half_weights_capped(uint32_t s_at, int half_til
                 a.y = mask >> (i + 1) & 1 ? a.y : 0.0f;
             }
             a = unpack2(mul2(pack2(a.x, a.y), fk2));
-            a = unpack2(add2(pack2(ex2(fminf(a.x, 60.0f)), ex2(fminf(a.y, 60.0f))), one));
+            a = unpack2(add2(pack2(ex2(min_nan(a.x, 60.0f)), ex2(min_nan(a.y, 60.0f))), one));
             const float r = rcp(a.x * a.y);
             const float2 w = unpack2(fma2(mul2(pack2(r, r), pack2(a.y, a.x)), m2c, c2));
             float2 z = make_float2(ex2(w.x), ex2(w.y));

@@ -78,6 +78,13 @@ __device__ __forceinline__ float rcp(float x)
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// The smaller of the two; NaN where either is (fminf would give the other).
+__device__ __forceinline__ float min_nan(float a, float b)
+{
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
 __device__ __forceinline__ uint64_t pack2(float lo, float hi)
 {
     uint64_t d;
@@ -139,8 +146,8 @@ __device__ __forceinline__ int q_exponent(float top)
 }
 __device__ __forceinline__ float pow2i(int x) { return __uint_as_float((uint32_t)(x + 127) << 23); }
 
-// The factor of a q row whose largest magnitude is top: 2^q_exponent, or NaN for a row that holds an
-// infinity, which makes the whole row NaN as the formula does.
+// The factor of a q row whose largest magnitude is top: 2^q_exponent, or NaN for a row that holds an infinity:
+// its scores, and with them its output, are NaN, capped or not, as are those of a row that holds a NaN.
 __device__ __forceinline__ float q_factor(float top)
 {
     return top < CUDART_INF_F ? pow2i(q_exponent(top)) : CUDART_NAN_F;

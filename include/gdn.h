@@ -541,7 +541,8 @@ size_t gdn_attn_workspace_bytes(const gdn_attn_dims *dims, int32_t prefill);
  *   s_j = scale * (q . k_j);  s_j = softcap * tanh(s_j / softcap) if softcap > 0;
  *   seen: j <= p, j < kv_len, and j > p - window if window > 0;
  *   out = sum_seen e^(s_j - max s) v_j / sum_seen e^(s_j - max s).
- * A row that sees nothing (padding) gives zeros.
+ * A row that sees nothing (padding) gives zeros, whatever its q holds. A row whose q holds a NaN or an infinity gives
+ * NaN in every dimension, with any softcap; the other rows' results stand.
  *   q    bf16 rows q_stride elements apart (16-byte aligned, a multiple of 16
  *        bytes apart), first Hq*128 used; already rotated (gdn_attn_append)
  *   out  bf16 [n_tokens][Hq][128] dense, rounded to nearest even
