@@ -707,12 +707,13 @@ size_t gdn_attn_workspace_bytes(const gdn_attn_dims *dims, int32_t prefill)
 {
     if (check_attn_dims(dims) != GDN_OK)
         return 0;
-    const int max_q = dims->max_q < dims->n_tokens ? dims->max_q : dims->n_tokens;
-    const int64_t rows = (int64_t)(dims->n_q_heads / dims->n_kv_heads) * max_q;
-    if (!prefill && rows > gdn::attn::kMaxDecodeRows)
+    if (prefill)
+        return gdn::attn::prefill_workspace_bytes(gdn::sm_count());
+    const int64_t G = dims->n_q_heads / dims->n_kv_heads, most = gdn::attn::kMaxDecodeRows;
+    if (G * (dims->max_q < dims->n_tokens ? dims->max_q : dims->n_tokens) > most)
         return 0;
-    return prefill ? gdn::attn::prefill_workspace_bytes(gdn::sm_count())
-                   : gdn::attn::decode_workspace_bytes((int)rows, gdn::sm_count());
+    const int64_t rows = G * dims->max_q;
+    return gdn::attn::decode_workspace_for_up_to((int)(rows < most ? rows : most), gdn::sm_count());
 }
 
 gdn_status gdn_attn_decode(const void *q, int64_t q_stride, const gdn_kv_cache *cache,

@@ -50,7 +50,8 @@ struct AttnArgs {
 cudaError_t launch_append(const AppendArgs &a, bool bf16, cudaStream_t s);
 cudaError_t launch_decode(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_prefill(const AttnArgs &a, cudaStream_t s);
-size_t decode_workspace_bytes(int rows, int sms);
+size_t decode_workspace_bytes(int rows, int sms);        // what a call of that many rows uses
+size_t decode_workspace_for_up_to(int rows, int sms);   // the most that any call of up to that many uses
 size_t prefill_workspace_bytes(int sms);
 cudaError_t take_append_error(int *code);
 cudaError_t take_decode_error(int *code);

@@ -703,6 +703,13 @@ size_t decode_workspace_bytes(int rows, int sms)
     return part_bytes((size_t)most_ctas(rows, sms), (size_t)rows);
 }
 
+// Calls of up to 16 rows run two CTAs an SM, and so can use more than those of a few rows more.
+size_t decode_workspace_for_up_to(int rows, int sms)
+{
+    const size_t own = decode_workspace_bytes(rows, sms), few = decode_workspace_bytes(rows < 16 ? rows : 16, sms);
+    return own > few ? own : few;
+}
+
 cudaError_t launch_decode(const AttnArgs &args, cudaStream_t s)
 {
     AttnArgs a = args;

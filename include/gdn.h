@@ -530,7 +530,8 @@ gdn_status gdn_attn_append(const void *q, int64_t q_stride, const void *k, int64
 /*
  * Workspace bytes of gdn_attn_decode (prefill = 0) or gdn_attn_prefill
  * (prefill = 1); it depends on the heads, on max_q and on the current device's
- * number of SMs, not on the lengths, n_seq or n_tokens.
+ * number of SMs, not on the lengths, n_seq or n_tokens. It never shrinks as max_q
+ * grows: a workspace for the most tokens serves calls of fewer.
  * Returns 0 for invalid or unsupported dims.
  */
 size_t gdn_attn_workspace_bytes(const gdn_attn_dims *dims, int32_t prefill);
