@@ -130,6 +130,16 @@ class AttnDims:
         object.__setattr__(self, "_ref", _ct.byref(self._c))
 
 
+def _device_of(*tensors) -> int | None:
+    """Index of the CUDA device that a handle's tensors (found to be on one device) are on; None for raw addresses."""
+    return next((t.get_device() for t in tensors if not isinstance(t, int)), None)
+
+
+def _elsewhere(name: str, has: int, dev: int):
+    return ValueError(f"{name}: its tensors are on cuda:{has}, the current device is "
+                      + (f"cuda:{dev}" if dev >= 0 else "none"))
+
+
 class KvCache:
     """A paged key/value cache (see gdn_kv_cache in include/gdn.h): codes k and v
     [n_pages][n_kv_heads][page_size][128] (float8_e4m3fn, or uint8), scales [n_pages][n_kv_heads]
@@ -152,10 +162,13 @@ class KvCache:
                 raise ValueError("cache.page_table: expected [n_seq][max_pages]")
             self._shape = (*k.shape, *page_table.shape)
         self._ref = _ct.byref(self._c)
+        self._device = _device_of(k, v, k_scale, v_scale, page_table)
         self._fits = None
 
-    def _for(self, dims: AttnDims):
-        """The C struct, once the tensors are known to be of the sizes in dims."""
+    def _for(self, dims: AttnDims, dev: int | None = None):
+        """The C struct, once the tensors are known to be of the sizes in dims and on CUDA device dev."""
+        if self._device != dev and self._device is not None and dev is not None:
+            raise _elsewhere("cache", self._device, dev)
         if self._fits is not dims:
             want = (dims.n_pages, dims.n_kv_heads, dims.page_size, dims.head_dim, dims.n_seq, dims.max_pages)
             if self._shape is not None and self._shape != want:
@@ -167,14 +180,22 @@ class KvCache:
 
 class Rope:
     """Position rotation table (see gdn_rope): cos and sin [n_positions][rotary_dim / 2] float32."""
+    _device = None
 
     def __init__(self, cos, sin, interleaved: bool = False):
         if cos.dim() != 2 or cos.shape != sin.shape:
             raise ValueError("rope: expected cos and sin of one shape [n_positions][rotary_dim / 2]")
         self.cos, self.sin, self.interleaved = cos, sin, bool(interleaved)
+        self._device = _device_of(cos, sin)
         self._c = _CRope(_dev(cos, "rope.cos", _F32), _dev(sin, "rope.sin", _F32), cos.shape[0],
                          2 * cos.shape[1], int(self.interleaved), 0)
         self._ref = _ct.byref(self._c)
+
+    def _on(self, dev: int):
+        """The C struct, once the tensors are known to be on CUDA device dev."""
+        if self._device != dev and self._device is not None:
+            raise _elsewhere("rope", self._device, dev)
+        return self._ref
 
     @classmethod
     def table(cls, n_positions: int, rotary_dim: int, base: float = 10000.0, interleaved: bool = False,
@@ -618,8 +639,8 @@ def attn_append(q, k, v, cache: KvCache, q_start, kv_len, rope: Rope, q_out, dim
     qp, qs = _rows(q, "q", same, n, hq, dev)
     op, _ = _rows(q_out, "q_out", _BF16_DT, n, hq, dev, True)
     status = (_lib or load()).gdn_attn_append(
-        qp, qs, kp, ks, vp, vs, GDN_BF16 if same == _BF16_DT else GDN_F32, cache._for(dims),
-        _counts(q_start, "q_start", dims.n_seq + 1, dev), _counts(kv_len, "kv_len", dims.n_seq, dev), rope._ref, op,
+        qp, qs, kp, ks, vp, vs, GDN_BF16 if same == _BF16_DT else GDN_F32, cache._for(dims, dev),
+        _counts(q_start, "q_start", dims.n_seq + 1, dev), _counts(kv_len, "kv_len", dims.n_seq, dev), rope._on(dev), op,
         dims._ref, handle)
     if status:
         _check(status, "gdn_attn_append")
@@ -646,7 +667,7 @@ def _attend(prefill: bool, q, cache, q_start, kv_len, out, dims, scale, softcap,
     elif not workspace.is_contiguous() or workspace.get_device() != dev:
         _ptr(workspace)
     status = (lib.gdn_attn_prefill if prefill else lib.gdn_attn_decode)(
-        qp, qs, cache._for(dims), starts, lens, op, dims._ref, 128 ** -0.5 if scale is None else scale, softcap,
+        qp, qs, cache._for(dims, dev), starts, lens, op, dims._ref, 128 ** -0.5 if scale is None else scale, softcap,
         window, workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle)
     if status:
         _check(status, "gdn_attn_prefill" if prefill else "gdn_attn_decode")
