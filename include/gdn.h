@@ -514,9 +514,9 @@ typedef struct gdn_rope {
  * Per page and KV head: the scale becomes the larger of what it was (unless
  * this call writes the page's slot 0) and the smallest power of two s with
  * max |new value| <= 448 s; when it grows, the page's other codes move to it;
- * new codes are value / s rounded to nearest even. An infinite key or value is
- * held as +-448 s and a NaN as 0 (neither counts for s), and either sets bit
- * 512 of the device error word, so that one bad row cannot poison a page.
+ * new codes are value / s rounded to nearest even. An infinite key (as rotated) or
+ * value is held as +-448 s and a NaN as 0 (neither counts for s), and either sets
+ * bit 512 of the device error word, so that one bad row cannot poison a page.
  * Sequences that share a page may not append to it in one call.
  * Errors: INVALID_ARG (null, sizes, strides, alignment, one of q and q_out
  * NULL), UNSUPPORTED (head_dim, page_size, G, rotary_dim).
