@@ -296,7 +296,9 @@ gdn_status attention(const void *q, int64_t q_stride, const gdn_kv_cache *cache,
     a.q_stride = q_stride;
     a.out = out;
     a.scale = scale;
-    a.softcap = softcap;
+    // Caps at the ends of the range divide by numbers that 32 bits do not hold. Below 1e-30 every capped score is 0
+    // as far as a weight can tell; above 1e36 no score that a softmax can tell from others is capped.
+    a.softcap = softcap == 0.0f ? 0.0f : fminf(fmaxf(softcap, 1e-30f), 1e36f);
     a.window = window;
     a.ws = static_cast<uint8_t *>(workspace);
     a.wait_ns = gdn::kDefaultWaitNs;
