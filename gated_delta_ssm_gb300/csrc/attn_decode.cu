@@ -377,7 +377,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
                               ((u ^ (r & 7)) << 4),
                           C::kRowBytes, v, q_factor(top));
                 if (u == 0) {
-                    sh.f[par][r] = A.scale * kLog2e * pow2i(-q_exponent(top));
+                    sh.f[par][r] = A.scale * (0.5f * kLog2e) * pow2i(1 - q_exponent(top));   // halved: it may be huge
                     sh.limit[par][r] = live ? w.first + tok : -1;
                 }
             }

@@ -627,7 +627,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
         const int per_tile = kTile >> page_shift;
         const int G = B.G, inv_G = 65536 / G + 1;   // y / G = y * inv_G >> 16 for y below 4096
         const float cap2 = A.softcap * kLog2e, inv_cap2 = CAP == kAnyCap ? 1.0f / cap2 : 0.0f;
-        const float f_scale = fabsf(A.scale) * kLog2e, sign = A.scale < 0.0f ? -1.0f : 1.0f;
+        const float f_scale = fabsf(A.scale) * (0.5f * kLog2e), sign = A.scale < 0.0f ? -1.0f : 1.0f;
         int c = 0;
         Seg &w = sh.now[warp - 4];   // in shared memory: the loop over tiles has no registers to spare for it
         float ref = 0.0f, l = 0.0f;
@@ -675,7 +675,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                     __syncwarp();   // the row is read before it is overwritten
                     store_q16(at_row + ((u ^ (rr & 7)) << 4), kTileBytes, v, sign * q_factor(top));
                     if (u == 0)
-                        sh.f[m][rr] = f_scale * pow2i(-q_exponent(top));
+                        sh.f[m][rr] = f_scale * pow2i(1 - q_exponent(top));
                 }
                 tc::fence_smem_to_async();
                 __syncwarp();

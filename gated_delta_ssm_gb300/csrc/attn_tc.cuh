@@ -139,10 +139,11 @@ __device__ __forceinline__ void load_q16(const __nv_bfloat16 *p, float (&v)[16])
     unpack_q16(a, b, v);
 }
 
-// x with 2^x top in [128, 256) (0 for top = 0); at most 126, so that 2^x stays finite.
+// x with 2^x top in [128, 256) (1 for top = 0: the factor of its scores, 0.72 scale, is finite for any scale); at
+// most 126, so that 2^x stays finite.
 __device__ __forceinline__ int q_exponent(float top)
 {
-    return top > 0.0f ? min(126, 134 - (int)(__float_as_uint(top) >> 23)) : 0;
+    return top > 0.0f ? min(126, 134 - (int)(__float_as_uint(top) >> 23)) : 1;
 }
 __device__ __forceinline__ float pow2i(int x) { return __uint_as_float((uint32_t)(x + 127) << 23); }
 

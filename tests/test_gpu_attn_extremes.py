@@ -31,3 +31,10 @@ def _run(form, scale=SCALE, std=1.0, zero_rows=(), **kw):
 @pytest.mark.parametrize("softcap", [1.5e-45, 1e-39, 1e-30, 1e-7, 55.4, 55.5, 1e20, 2.9e38, 3e38])
 def test_caps(form, softcap):
     _run(form, softcap=softcap, zero_rows=(1,))
+
+
+@pytest.mark.parametrize("form", ["decode", "prefill"])
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+@pytest.mark.parametrize("scale,std", [(3e38, 1e-36), (-3e38, 1e-36), (1e-38, 1e38 / 8), (0.0, 1e30)])
+def test_scales(form, softcap, scale, std):
+    _run(form, scale=scale, std=std, softcap=softcap, zero_rows=(1,))
