@@ -717,7 +717,7 @@ cudaError_t launch_decode(const AttnArgs &args, cudaStream_t s)
     if (a.window == 0 || a.window > kNoWindow)
         a.window = kNoWindow;
     const int rows = b.G * b.max_q, most = most_ctas(rows, a.sm_count);
-    if (most_units(b, kMaxDecodeRows, kOver) > 2e9)
+    if (most_units(b, kMaxDecodeRows, kOver) > kMostUnits)
         return cudaErrorInvalidConfiguration;
     const int64_t tiles = ((int64_t)b.max_pages * b.P + kTile - 1) / kTile, blocks = (int64_t)b.n_seq * b.Hkv;
     const int64_t units = (tiles + kOver) * blocks;

@@ -909,7 +909,7 @@ cudaError_t launch_prefill(const AttnArgs &args, cudaStream_t s)
     const Batch &b = a.b;
     if (a.window == 0 || a.window > kNoWindow)
         a.window = kNoWindow;
-    if (most_units(b, kRows, kOver) > 2e9)
+    if (most_units(b, kRows, kOver) > kMostUnits)
         return cudaErrorInvalidConfiguration;
     const int64_t tiles = ((int64_t)b.max_pages * b.P + kTile - 1) / kTile;
     const int64_t blocks = ((int64_t)b.max_q * b.G + kRows - 1) / kRows * b.Hkv * b.n_seq;

@@ -48,7 +48,14 @@ struct ShareShared {
     Seq start_seq;
 };
 
-// Units are 32-bit numbers: most_units bounds them on the host. Of `total` units, the first `more` of n_cta
+// Units are 32-bit numbers: most_units bounds them on the host, by kMostUnits, for sequences that share no rows.
+// Where q_start runs backwards, valid sequences can share rows and their units can be more. So sums stop at the
+// largest number, and of more than kMostUnits units none is done: nothing could be found by a sum that wrapped.
+// (The entry that runs backwards is reported by clear_empty.)
+constexpr int kMostUnits = 2000000000;
+__device__ __forceinline__ int add_units(int a, int b) { return (int)min((unsigned)a + (unsigned)b, 0x7fffffffu); }
+
+// Of `total` units, the first `more` of n_cta
 // shares take each + 1, the others `each`: one short division for all that a walk needs.
 struct Share {
     int n_cta, each, more;
@@ -138,7 +145,7 @@ __device__ __forceinline__ Share find_share(const AttnArgs &A, ShareShared<THREA
 #pragma unroll 2
     for (int i = 0; i < per; ++i)
         if (first_b + i < B.n_seq)
-            mine += head_tiles<ROWS>(A, first_b + i, sub, g, blocks, longest);
+            mine = add_units(mine, head_tiles<ROWS>(A, first_b + i, sub, g, blocks, longest));
     for (int m = 1; m < g; m <<= 1) {
         mine += __shfl_xor_sync(0xffffffffu, mine, m);
         blocks += __shfl_xor_sync(0xffffffffu, blocks, m);
@@ -155,15 +162,15 @@ __device__ __forceinline__ Share find_share(const AttnArgs &A, ShareShared<THREA
         }
         split = longest > WHOLE || (int64_t)all * B.Hkv > gridDim.x;
     }
-    mine = split ? mine + OVER * blocks : blocks;
-    const int one_head = mine;
-    mine = sub == 0 ? mine * B.Hkv : 0;
+    const int64_t head = split ? mine + (int64_t)OVER * blocks : blocks;
+    const int one_head = (int)head;   // where it is used, of one sequence
+    mine = sub == 0 ? (int)min(head * B.Hkv, (int64_t)0x7fffffff) : 0;
     int incl = mine;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
         const int up = __shfl_up_sync(0xffffffffu, incl, m);
         if (lane >= m)
-            incl += up;
+            incl = add_units(incl, up);
     }
     Share r;
     int total = __shfl_sync(0xffffffffu, incl, 31);
@@ -174,10 +181,12 @@ __device__ __forceinline__ Share find_share(const AttnArgs &A, ShareShared<THREA
         total = 0;
 #pragma unroll 1
         for (int i = 0; i < threads / 32; ++i) {
-            incl += i < warp ? sh.warp_sum[i] : 0;
-            total += sh.warp_sum[i];
+            incl = add_units(incl, i < warp ? sh.warp_sum[i] : 0);
+            total = add_units(total, sh.warp_sum[i]);
         }
     }
+    if (total > kMostUnits)
+        total = 0;
     const int c = blockIdx.x;
     r.n_cta = min((int)gridDim.x, total);
     r.each = r.n_cta > 0 ? total / r.n_cta : 1;

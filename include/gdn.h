@@ -459,7 +459,8 @@ gdn_status gdn_prefill_chunked_noalloc(float *state, float *conv_state, const vo
  *   sequence whose entries are out of range, or a page-table entry outside
  *   0 .. n_pages - 1, sets bit 256 of the device error word
  *   (gdn_check_device). Such a sequence is skipped (its outputs are not
- *   written); tokens of such a page are not appended, and not seen.
+ *   written); tokens of such a page are not appended, and not seen. Where q_start
+ *   runs backwards, an attention call may skip the other sequences too.
  *
  * DRAFTS  To drop rejected draft tokens, lower kv_len in the next call; the
  *   next append overwrites their slots. The page keeps the scale that they may
