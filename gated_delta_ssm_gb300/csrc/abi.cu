@@ -681,7 +681,8 @@ gdn_status gdn_attn_append(const void *q, int64_t q_stride, const void *k, int64
     if (!valid_dtype(act_dtype) || !rope || rope->reserved != 0 || rope->n_positions < 0 ||
         rope->rotary_dim < 0 || rope->rotary_dim > gdn::kD || (rope->interleaved & ~1) != 0)
         return GDN_ERR_INVALID_ARG;
-    if (rope->rotary_dim > 0 && (!rope->cos || !rope->sin || !aligned(rope->cos, 16) || !aligned(rope->sin, 16)))
+    if (rope->rotary_dim > 0 && (!rope->cos || !rope->sin || !aligned(rope->cos, 16) || !aligned(rope->sin, 16) ||
+                                 rope->n_positions < 1))   // a padding row is turned by position 0
         return GDN_ERR_INVALID_ARG;
     const size_t es = act_size(act_dtype);
     const int64_t kv = (int64_t)a.b.Hkv * gdn::kD;

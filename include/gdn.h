@@ -497,7 +497,7 @@ typedef struct gdn_kv_cache {
 typedef struct gdn_rope {
     const float *cos;     /* [n_positions][rotary_dim / 2] */
     const float *sin;
-    int32_t n_positions;  /* every position of a call must be below it */
+    int32_t n_positions;  /* >= 1 (rotary_dim 0: any); every position of a call must be below it */
     int32_t rotary_dim;   /* a multiple of 16, <= 128 */
     int32_t interleaved;  /* 0 or 1 */
     int32_t reserved;     /* must be 0 */
