@@ -661,7 +661,7 @@ def _attend(prefill: bool, q, cache, q_start, kv_len, out, dims, scale, softcap,
     lib = _lib or load()
     if workspace is None:
         nbytes = max(attn_workspace_bytes(dims, prefill), 16)
-        workspace = _torch.empty(nbytes, dtype=_torch.uint8, device=q.device)
+        workspace = _torch.empty(nbytes, dtype=_torch.uint8, device="cuda")
         if stream is not None:   # its memory is not handed out again before that stream is done with it
             workspace.record_stream(_torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
     elif not workspace.is_contiguous() or workspace.get_device() != dev:
