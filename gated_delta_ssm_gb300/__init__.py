@@ -360,6 +360,19 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream
 
 
+def _own_workspace(nbytes: int, stream):
+    """Device memory for one call, from the pool of the call's stream: what that stream did with it before, and what
+    it is handed out for after the call, are in the stream's order."""
+    import torch
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+
+
 def _check(status: int, fn: str):
     if status != GDN_OK:
         detail = load().gdn_last_cuda_error().decode() if status == GDN_ERR_CUDA else ""
@@ -476,9 +489,7 @@ def prefill_chunked(state, conv_state, x, z, alpha, beta_logit, params: Params, 
     bytes; when None, one is allocated with torch for this call."""
     cd, cp = dims.c(), params.c()
     if workspace is None:
-        import torch
-        nbytes = prefill_workspace_bytes(dims, n_tokens, chunk)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=x.device)
+        workspace = _own_workspace(max(prefill_workspace_bytes(dims, n_tokens, chunk), 16), stream)
     ws = _ptr(workspace)
     ws_bytes = workspace.numel() * workspace.element_size()
     _check(load().gdn_prefill_chunked(_dev(state, "state", _F32), _dev(conv_state, "conv_state", _F32),
@@ -661,9 +672,7 @@ def _attend(prefill: bool, q, cache, q_start, kv_len, out, dims, scale, softcap,
     lib = _lib or load()
     if workspace is None:
         nbytes = max(attn_workspace_bytes(dims, prefill), 16)
-        workspace = _torch.empty(nbytes, dtype=_torch.uint8, device="cuda")
-        if stream is not None:   # its memory is not handed out again before that stream is done with it
-            workspace.record_stream(_torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+        workspace = _own_workspace(nbytes, stream)
     elif not workspace.is_contiguous() or workspace.get_device() != dev:
         _ptr(workspace)
     status = (lib.gdn_attn_prefill if prefill else lib.gdn_attn_decode)(
