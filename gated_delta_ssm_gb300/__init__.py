@@ -124,6 +124,9 @@ class AttnDims:
     page_size: int = 64
 
     def __post_init__(self):
+        for name, value in vars(self).items():
+            if not -1 << 31 <= value < 1 << 31:
+                raise ValueError(f"{name}: {value} is not a 32-bit number")
         object.__setattr__(self, "_c", _CAttnDims(
             self.n_seq, self.n_q_heads, self.n_kv_heads, self.head_dim, self.page_size, self.n_pages,
             self.max_pages, self.n_tokens, self.max_q, 0))
@@ -677,7 +680,7 @@ def _attend(prefill: bool, q, cache, q_start, kv_len, out, dims, scale, softcap,
         _ptr(workspace)
     status = (lib.gdn_attn_prefill if prefill else lib.gdn_attn_decode)(
         qp, qs, cache._for(dims, dev), starts, lens, op, dims._ref, 128 ** -0.5 if scale is None else scale, softcap,
-        window, workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle)
+        min(max(window, -1), 0x7fffffff), workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle)
     if status:
         _check(status, "gdn_attn_prefill" if prefill else "gdn_attn_decode")
 
