@@ -330,6 +330,7 @@ __device__ __forceinline__ Seg take_seg(Ring &ring, int k, W wait, const volatil
     Seg q = ring.seg[slot];
     if (__any_sync(0xffffffffu, *abort != 0))
         q.nt = 0;
+    __syncwarp();   // every lane has read the slot (a vote orders no memory)
     if ((threadIdx.x & 31) == 0)
         tc::mbar_arrive(tc::smem_addr(&ring.free[slot]));
     return q;
