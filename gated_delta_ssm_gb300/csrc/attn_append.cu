@@ -267,6 +267,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) append_kernel(const __grid_cons
         const Seq s = load_seq(B, b);
         if (tok >= s.n || (s.L > A.n_positions && A.rot > 0))
             return;                   // the cache groups report positions past the table
+        GDN_CHECK(g_append_error, b < B.n_seq && s.row0 + tok < B.n_tokens && h0 < B.Hq &&
+                                      (A.rot == 0 || max(s.L - s.n + tok, 0) < A.n_positions));
         const T *src = static_cast<const T *>(A.q) + (int64_t)(s.row0 + tok) * A.q_stride + h0 * kHd;
         __nv_bfloat16 *dst =
             static_cast<__nv_bfloat16 *>(A.q_out) + ((int64_t)(s.row0 + tok) * B.Hq + h0) * kHd;
@@ -317,6 +319,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) append_kernel(const __grid_cons
     const int p1 = min(s.L, (blk + 1) << page_shift);
     if (s.n == 0 || p0 >= p1)
         return;
+    GDN_CHECK(g_append_error, b < B.n_seq && h < B.Hkv && blk >= 0 && blk < B.max_pages && p1 - p0 <= PASSES * kTok &&
+                                  s.row0 + s.n - s.L + p0 >= s.row0 && s.row0 + s.n - s.L + p1 <= B.n_tokens &&
+                                  (A.rot == 0 || p1 <= A.n_positions));
     const int page = __ldg(B.page_table + (int64_t)b * B.max_pages + blk);
     const T *src = static_cast<const T *>(which ? A.v : A.k);
     const int64_t stride = which ? A.v_stride : A.k_stride;

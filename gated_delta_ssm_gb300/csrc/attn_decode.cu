@@ -240,12 +240,14 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
             const Seg w = take_seg(sh.ring, k, wait, &sh.abort);
             if (w.nt == 0)
                 break;
+            GDN_CHECK(g_attn_decode_error, seg_in_range(A, w));
             const int32_t *table = B.page_table + (int64_t)w.b * B.max_pages;
             const int pg_lo = w.lo >> page_shift, pg_hi = w.hi >> page_shift;
             auto page_of = [&](int t) {   // this lane's page of the tile, -1: none wanted, -2: bad
                 const int pg = (w.kt + t) * per_tile + lane;
                 if (t >= w.nt || lane >= per_tile || pg < pg_lo || pg > pg_hi)
                     return -1;
+                GDN_CHECK(g_attn_decode_error, pg >= 0 && pg < B.max_pages);
                 const int p = __ldg(table + pg);
                 return p >= 0 && p < B.n_pages ? p : -2;
             };
@@ -361,6 +363,8 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
             for (int r = r4; r < ((R + 3) & ~3); r += 4) {
                 const int tok = r * inv_G >> 16, g = r - tok * B.G;
                 const bool live = tok < w.n;
+                GDN_CHECK(g_attn_decode_error,
+                          r < NR && (!live || (w.row0 + tok < B.n_tokens && w.h * B.G + g < B.Hq)));
                 float v[16] = {};
                 if (live)
                     load_q16(static_cast<const __nv_bfloat16 *>(A.q) + (int64_t)(w.row0 + tok) * A.q_stride +
@@ -413,6 +417,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
                 const int j = (w.kt + t) * kTile + t128;
                 if (t >= w.nt || j < w.lo || j > w.hi)
                     return -1;
+                GDN_CHECK(g_attn_decode_error, j >= 0 && j >> page_shift < B.max_pages);
                 const int p = __ldg(table + (j >> page_shift));
                 return p >= 0 && p < B.n_pages ? p : -1;
             };
@@ -634,6 +639,7 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
             float *part = parts + (size_t)(2 * blockIdx.x + (w.begins ? 1 : 0)) * R * kPartRow;
 #pragma unroll 1
             for (int r = wq; r < rows; r += 4) {
+                GDN_CHECK(g_attn_decode_error, r < R && w.row0 + r / B.G < B.n_tokens && seg_in_range(A, w));
                 const float at = sh.o_ref[r];
                 float l = 0.0f;
 #pragma unroll

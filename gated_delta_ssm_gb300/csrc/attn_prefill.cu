@@ -485,12 +485,14 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                 const Seg w = take_seg(sh.ring, k, wait, &sh.abort);
                 if (w.nt == 0)
                     break;
+                GDN_CHECK(g_attn_prefill_error, seg_in_range(A, w));
                 const int32_t *table = B.page_table + (int64_t)w.b * B.max_pages;
                 const int pg_lo = w.lo >> page_shift, pg_hi = w.hi >> page_shift;
                 auto page_of = [&](int t) {   // this lane's page of the tile, -1: none wanted, -2: bad
                     const int pg = (w.kt + t) * per_tile + lane;
                     if (t >= w.nt || lane >= per_tile || pg < pg_lo || pg > pg_hi)
                         return -1;
+                    GDN_CHECK(g_attn_prefill_error, pg >= 0 && pg < B.max_pages);
                     const int p = __ldg(table + pg);
                     return p >= 0 && p < B.n_pages ? p : -2;
                 };
@@ -641,6 +643,8 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                 const uint32_t at = kQAt + 2 * m * kTileBytes;
                 const int row_w = (warp & 3) * 32;
                 const int y = nx.rem0 + m * 128 + row, dt = y * inv_G >> 16, t = nx.tok0 + dt;
+                GDN_CHECK(g_attn_prefill_error, seg_in_range(A, nx) && y < 4096 && y - dt * G < G &&
+                                                    (t >= nx.n || nx.row0 + t < B.n_tokens));
                 const uint64_t mine = t < nx.n ? reinterpret_cast<uint64_t>(
                                                      static_cast<const __nv_bfloat16 *>(A.q) +
                                                      (int64_t)(nx.row0 + t) * A.q_stride + (nx.h * G + y - dt * G) * kHd)
@@ -691,6 +695,8 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                 uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(A.out) +
                                                        ((int64_t)(w.row0 + tok) * B.Hq + w.h * G + head) * kHd);
                 float *part = parts + ((size_t)(2 * blockIdx.x + (w.begins ? 1 : 0)) * kRows + x) * kPartRow;
+                GDN_CHECK(g_attn_prefill_error, seg_in_range(A, w) && x < kRows && head >= 0 && head < G &&
+                                                    (!live || w.row0 + tok < B.n_tokens));
 #pragma unroll 1
                 for (int q4 = 0; q4 < 4; ++q4) {
                     uint32_t v[32];
@@ -714,7 +720,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                     }
                 }
                 if (joined) {
-                    *reinterpret_cast<float2 *>(part + kHd) = make_float2(l, l == 0.0f ? kNoRef : ref);   // NaN keeps ref
+                    *reinterpret_cast<float2 *>(part + kHd) = make_float2(l, l == 0.0f ? kNoRef : ref);
                     if (w.begins && x == 0)
                         meta[blockIdx.x] = {w.b, w.h, w.blk, w.last_cta, 1, {}};
                 }
@@ -810,6 +816,7 @@ attn_prefill_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ 
                 const int j = (w.kt + t) * kTile + t128;
                 if (t >= w.nt || j < w.lo || j > w.hi)
                     return -1;
+                GDN_CHECK(g_attn_prefill_error, j >= 0 && j >> page_shift < B.max_pages);
                 const int p = __ldg(table + (j >> page_shift));
                 return p >= 0 && p < B.n_pages ? p : -1;
             };

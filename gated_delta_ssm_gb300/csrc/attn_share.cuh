@@ -336,6 +336,18 @@ __device__ __forceinline__ Seg take_seg(Ring &ring, int k, W wait, const volatil
     return q;
 }
 
+// For GDN_CHECK: a segment lies in the batch. Everything that a role indexes with is one of its fields, or a thread's
+// place within rows, tile or page beside them.
+__device__ __forceinline__ bool seg_in_range(const AttnArgs &A, const Seg &w)
+{
+    const Batch &B = A.b;
+    return w.b >= 0 && w.b < B.n_seq && w.h >= 0 && w.h < B.Hkv && w.row0 >= 0 && w.n >= 1 && w.n <= B.max_q &&
+           w.row0 + w.n <= B.n_tokens && w.lo >= 0 && w.hi >= w.lo && w.hi < B.max_pages * B.P &&
+           w.kt >= w.lo / kTile && w.kt + w.nt - 1 <= w.hi / kTile && w.blk >= 0 && w.blk < w.n * B.G &&
+           w.tok0 * B.G + w.rem0 == w.blk && w.rem0 >= 0 && w.rem0 < B.G && w.last_cta >= (int)blockIdx.x &&
+           w.last_cta < (int)gridDim.x && (w.begins || blockIdx.x > 0);
+}
+
 // Sequences without keys: nobody else looks at them. Their rows are zero, and bad entries are reported.
 __device__ __forceinline__ void clear_empty(const AttnArgs &A, int *error)
 {
