@@ -35,6 +35,8 @@
 // one or two groups of four warps hold a key per thread and turn scores into
 // weights, and the last four warps hold a dimension per thread and join the
 // products.
+#include <cfloat>
+
 #include "attn_share.cuh"
 #include "attn_tc.cuh"
 #include "cluster.cuh"
@@ -655,9 +657,11 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
                                               ((int64_t)(w.row0 + tok) * B.Hq + w.h * B.G + g) * kHd)[lane] =
                         make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
                 } else {
+                    // l counts 2^-e for values of 2^e: over pages of zeros alone (e = -100) it can be infinite,
+                    // and the join would turn that into NaN where it scales the part to nothing
                     *reinterpret_cast<float4 *>(part + r * kPartRow + 4 * lane) = x;
                     if (lane == 0)
-                        *reinterpret_cast<float2 *>(part + r * kPartRow + kHd) = make_float2(l, at);
+                        *reinterpret_cast<float2 *>(part + r * kPartRow + kHd) = make_float2(min_nan(l, FLT_MAX), at);
                 }
             }
             if (!w.whole && w.begins && d == 0)

@@ -1,0 +1,60 @@
+"""Values of zero, under scores that rise steeply."""
+import pytest
+
+from tests._attn import Batch, check
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import gated_delta_ssm_gb300 as gdn  # noqa: E402
+
+
+def _run(form, t, scale, **kw):
+    out = torch.full((t.N, t.Hq, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    (gdn.attn_decode if form == "decode" else gdn.attn_prefill)(
+        t.q, t.cache(), t.d["q_start"], t.d["kv_len"], out, t.dims(), scale=scale, **kw)
+    torch.cuda.synchronize()
+    assert gdn.check_device() == 0
+    return out
+
+
+def _steps(ns, lens, Hq, steps, seed=0):
+    """Every key of tile i scores steps[i]: keys of one value in all dimensions, q of ones, scale 1 / 128."""
+    t = Batch(ns, lens, Hq, 1, 64, seed=seed)
+    for b in range(t.B):
+        for blk in range(-(-t.lens[b] // 64)):
+            v = float(steps(blk // 2))
+            t.k[t.table[b, blk]] = torch.tensor([v]).to(torch.float8_e4m3fn).view(torch.uint8).item()
+    t.ks[:] = 1.0
+    t.d["k"].copy_(torch.from_numpy(t.k)), t.d["ks"].copy_(torch.from_numpy(t.ks))
+    t.q = torch.ones(t.N, Hq, 128, dtype=torch.bfloat16, device="cuda")
+    return t
+
+
+def _values(t, exponent, zero=lambda blk: False):
+    """Values of pages of scale 2^exponent, zeros (as an append of zeros leaves them) in the pages that `zero` says."""
+    t.vs[:] = 2.0 ** exponent
+    for b in range(t.B):
+        for blk in range(-(-t.lens[b] // 64)):
+            if zero(blk):
+                t.v[t.table[b, blk]], t.vs[t.table[b, blk]] = 0, 2.0 ** -100
+    t.d["v"].copy_(torch.from_numpy(t.v)), t.d["vs"].copy_(torch.from_numpy(t.vs))
+
+
+@pytest.mark.parametrize("form", ["decode", "prefill"])
+def test_values_of_zero_everywhere(form):
+    # three steps of e^20 within each CTA's share, and shares e^192 apart
+    t = _steps([1], [131072], 1, lambda i: 20 * (i % 3) if i < 900 else 192)
+    _values(t, 0, zero=lambda blk: True)
+    assert not _run(form, t, 1 / 128).any()
+
+
+@pytest.mark.parametrize("form", ["decode", "prefill"])
+@pytest.mark.parametrize("top", [20, 40, 112])
+def test_pages_of_zeros_among_others(form, top):
+    t = _steps([1, 4], [40000, 900], 2, lambda i: top * (i % 3) / 2)
+    _values(t, -8, zero=lambda blk: blk % 4 == 1)
+    check(_run(form, t, 1 / 128), *t.expected(1 / 128))
