@@ -576,14 +576,15 @@ attn_decode_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ C
             for (int t = 0; t < w.nt; ++t, ++i) {
                 const int ob = i % C::kO;
                 wait(sh.coef_full[i & 3], (i >> 2) & 1);
-                // a (row, warp) pair per thread: its scale. The references lag: sums of 32 bits do not mind 2^60
+                // a (row, warp) pair per thread: its scale. The references lag, by 2^20 at most: sums of 32 bits do
+                // not mind, with values down to 2^-75 neither (l holds their reciprocals)
                 bool move = false;
 #pragma unroll
                 for (int e = 0; e < (4 * NR + 127) / 128; ++e) {
                     const int r = 32 * e + (d >> 2);
                     if (r < R) {
                         const float m = reinterpret_cast<const float *>(&sh.top[i & 3][r])[d & 3] - sh.o_ref[r];
-                        move |= m > 60.0f;
+                        move |= m > 20.0f;
                         reinterpret_cast<float *>(&sh.scale[i & 1][r])[d & 3] = ex2(m);
                     }
                 }

@@ -1,4 +1,5 @@
-"""Values of zero, under scores that rise steeply."""
+"""Values at the ends of the ranges that gdn.h states for the attention calls, under scores that rise steeply."""
+import numpy as np
 import pytest
 
 from tests._attn import Batch, check
@@ -58,3 +59,30 @@ def test_pages_of_zeros_among_others(form, top):
     t = _steps([1, 4], [40000, 900], 2, lambda i: top * (i % 3) / 2)
     _values(t, -8, zero=lambda blk: blk % 4 == 1)
     check(_run(form, t, 1 / 128), *t.expected(1 / 128))
+
+
+@pytest.mark.parametrize("exponent", [-75, -40, 0, 60, 100])
+@pytest.mark.parametrize("top", [20, 40, 112])
+def test_decode(exponent, top):
+    t = _steps([1, 4], [131072, 900], 2, lambda i: top * (i % 3) / 2)
+    _values(t, exponent)
+    out, (want, bound) = _run("decode", t, 1 / 128), t.expected(1 / 128)
+    check(out, want, bound)
+    assert np.abs(want).max() > 2.0 ** exponent      # nothing but rounding separates zeros from these
+
+
+@pytest.mark.parametrize("exponent", [-50, 0, 48])      # 448 * 2^48 * 6000 keys < 2^70
+@pytest.mark.parametrize("top", [20, 40, 112])
+def test_prefill(exponent, top):
+    t = _steps([300, 2], [6000, 1000], 2, lambda i: top * (i % 3) / 2)
+    _values(t, exponent)
+    check(_run("prefill", t, 1 / 128), *t.expected(1 / 128))
+
+
+@pytest.mark.parametrize("softcap", [30.0, 50.0, 55.0])
+@pytest.mark.parametrize("exponent", [-50, 0, 23])      # 448 * 2^23 * 6000 keys < 2^45
+@pytest.mark.parametrize("score", [-448, 448])
+def test_prefill_with_a_cap(softcap, exponent, score):
+    t = _steps([300, 2], [6000, 1000], 2, lambda i: score)
+    _values(t, exponent)
+    check(_run("prefill", t, 1 / 128, softcap=softcap), *t.expected(1 / 128, softcap))
