@@ -86,3 +86,19 @@ def test_prefill_with_a_cap(softcap, exponent, score):
     t = _steps([300, 2], [6000, 1000], 2, lambda i: score)
     _values(t, exponent)
     check(_run("prefill", t, 1 / 128, softcap=softcap), *t.expected(1 / 128, softcap))
+
+
+@pytest.mark.parametrize("form,P", [("decode", 16), ("decode", 64), ("prefill", 16)])
+@pytest.mark.parametrize("low,high", [(-75, -5), (-35, 35), (30, 100), (-50, 20)])
+def test_pages_of_very_different_scales(form, P, low, high):
+    if form == "prefill" and (low < -50 or high > 45):
+        pytest.skip("past the prefill's range")
+    t = Batch([1, 4], [9000, 900], 2, 1, P, seed=P)
+    t.make_q()
+    t.vs[:] = 2.0 ** np.where(t.rng.random(t.vs.shape) < 0.5, low, high)
+    t.d["vs"].copy_(torch.from_numpy(t.vs))
+    out = torch.zeros(t.N, t.Hq, 128, dtype=torch.bfloat16, device="cuda")
+    (gdn.attn_decode if form == "decode" else gdn.attn_prefill)(
+        t.q, t.cache(), t.d["q_start"], t.d["kv_len"], out, t.dims())
+    torch.cuda.synchronize()
+    check(out, *t.expected(128 ** -0.5))
