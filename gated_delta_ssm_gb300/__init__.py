@@ -131,6 +131,9 @@ class AttnDims:
             self.n_seq, self.n_q_heads, self.n_kv_heads, self.head_dim, self.page_size, self.n_pages,
             self.max_pages, self.n_tokens, self.max_q, 0))
         object.__setattr__(self, "_ref", _ct.byref(self._c))
+        # the sizes of the cache's tensors
+        object.__setattr__(self, "_cache", (self.n_pages, self.n_kv_heads, self.page_size, self.head_dim, self.n_seq,
+                                            self.max_pages))
 
 
 def _device_of(*tensors) -> int | None:
@@ -166,18 +169,14 @@ class KvCache:
             self._shape = (*k.shape, *page_table.shape)
         self._ref = _ct.byref(self._c)
         self._device = _device_of(k, v, k_scale, v_scale, page_table)
-        self._fits = None
 
     def _for(self, dims: AttnDims, dev: int | None = None):
         """The C struct, once the tensors are known to be of the sizes in dims and on CUDA device dev."""
         if self._device != dev and self._device is not None and dev is not None:
             raise _elsewhere("cache", self._device, dev)
-        if self._fits is not dims:
-            want = (dims.n_pages, dims.n_kv_heads, dims.page_size, dims.head_dim, dims.n_seq, dims.max_pages)
-            if self._shape is not None and self._shape != want:
-                raise ValueError(f"cache: sizes {self._shape}, dims say {want} "
-                                 "(n_pages, n_kv_heads, page_size, head_dim, n_seq, max_pages)")
-            self._fits = dims
+        if self._shape != dims._cache and self._shape is not None:
+            raise ValueError(f"cache: sizes {self._shape}, dims say {dims._cache} "
+                             "(n_pages, n_kv_heads, page_size, head_dim, n_seq, max_pages)")
         return self._ref
 
 

@@ -85,3 +85,12 @@ def test_raw_addresses_stay_unchecked(on):
     on(3)
     cache = gdn.KvCache(FAKE, FAKE, FAKE, FAKE, FAKE)
     assert ct.addressof(cache._for(DIMS, 3)._obj) == ct.addressof(cache._c)
+
+
+def test_the_sizes_are_looked_at_in_every_call():
+    cache = gdn.KvCache(*[FAKE] * 5)
+    cache._shape = (10, 2, 64, 128, 2, 4)
+    assert cache._for(DIMS) is cache._ref
+    cache._shape = (10, 2, 64, 128, 2, 5)
+    with pytest.raises(ValueError, match="cache: sizes"):
+        cache._for(DIMS)
