@@ -1,5 +1,5 @@
 // attn.h -- internal launch interface of the attention operators over the paged
-// 8-bit key/value cache, between the C ABI (abi_attn.cu) and the kernel files.
+// 8-bit key/value cache, between the C ABI (abi.cu) and the kernel files.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -21,8 +21,9 @@
 //
 // Measured: 4 x 8192 tokens, 16 q heads on 4, bf16: 74 us, 5.2 TB/s of the bytes it cannot do without. Its warps
 // wait for loads (5.6 of 12 cycles an issue); 64 registers, four CTAs of 256 threads an SM, measured best (three
-// CTAs: 76.7 us; 512 threads: 83 us; before the angles were shared by a token's heads: 102 us). A single token: the
-// call's 8 us on the host.
+// CTAs: 76.7 us; 512 threads: 83 us; before the angles were shared by a token's heads: 102 us). The same in float32:
+// 106 us, 5.5 TB/s, although its forms for more than four tokens a sequence spill (252 bytes a thread at pages of 16
+// and 32, about 360 at 64 and 128). A single token: the call's 8 us on the host.
 #include <cfloat>
 #include <cuda_fp8.h>
 

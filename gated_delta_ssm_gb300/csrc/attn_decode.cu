@@ -8,7 +8,7 @@
 // its columns. Both products read the cache's codes as they lie in shared
 // memory: nothing is converted. Q and P are each split into two e4m3 numbers,
 // hi + lo. A bf16 q row scaled by a power of two so that its largest value is
-// below 256 is hi + lo exactly (down to 2^-18 of that largest value); a weight
+// below 256 is hi + lo exactly (down to 2^-17 of that largest value); a weight
 // keeps 2^-8 of itself, as many bits as bf16 has.
 //   The key scale of a page and the value scale 2^e enter the exponent:
 // w = s f ks + e, P = 2^(w - max w + 8) <= 256, the maximum taken over the 32
@@ -26,9 +26,12 @@
 // Measured: 64 sequences of 800 to 8191 tokens, 32 q heads on 8, one token each:
 // 102 us, 5.6 TB/s (DRAM busy 71% of the time, the tensor pipe 8%). One sequence
 // of 131071 tokens, 4 KV heads: 42 us, of which about 8 pass before the first
-// tile is used and 5 in the join. 32 drafts of four tokens, cap 30, R = 32: 63 us,
-// bound by instructions (about 8200 warp instructions a tile); four groups of
-// softmax warps there take 70 us, two columns' loops unrolled 73 us.
+// tile is used and 5 in the join; between them the codes come at 4.7 TB/s, not the
+// memory's rate. 32 drafts of four tokens, cap 30, R = 32: 63 us. A tile there takes
+// about 8100 warp instructions, and issue slots are 43% busy: what is waited for is
+// the chain copy, scores, weights, output, join of a tile (loads 2.5, fixed latencies
+// 1.5, barriers 1.3 of 9.3 cycles an issue). Four groups of softmax warps there take
+// 70 us, two columns' loops unrolled 73 us.
 //
 // Roles of a CTA: warp 0 copies pages to shared memory, warp 1 issues the
 // products, warp 2 splits the q rows of the next segment, warp 3 walks the share,

@@ -22,9 +22,12 @@
 // Measured: 4 x 8192 tokens, 16 q heads on 4: 861 us, 1.28 PFLOP/s. The products
 // of a pair of tiles take 2051 cycles back to back; with the other roles' shared
 // memory traffic and the chain scores, weights, output they take 2800 to 3000.
-// 1024 tokens behind 32768, 32 heads on 4, cap 50: 622 us, bound by three
-// exponentials and a half reciprocal a score. Window 1000, 6 prompts: 84 us, where
-// about 12000 cycles a block for q and the output count for as much as its tiles.
+// 1024 tokens behind 32768, 32 heads on 4, cap 50: 624 us; two exponentials and half
+// a reciprocal a score keep their pipe 56% busy, the tensor pipe is at 37%, issue
+// slots at 55%: the rest is the chain's latency. Window 1000, 6 prompts: 84 us. A
+// block there is 9.4 tiles of 2800 to 3000 cycles and about 12000 cycles for q and
+// the output, 44 to 51 us for the 2.1 blocks a CTA gets; start, join and waits
+// between them are the rest, not taken apart further.
 // Loops are short on purpose: unrolled further, fetching instructions stalls them.
 //
 // Roles of a CTA (512 threads): warp 0 copies pages, warps 1 and 2 issue the

@@ -151,7 +151,8 @@ __device__ __forceinline__ Share find_share(const AttnArgs &A, ShareShared<THREA
         blocks += __shfl_xor_sync(0xffffffffu, blocks, m);
     }
     // Few short blocks go to a CTA each, whole: to split them would cost more in joining than it saves.
-    // (Counted by one warp only; a CTA-wide count is of more sequences than CTAs.)
+    // (Looked at where one warp counts; a batch of more than kFewSeqs sequences is always split, which costs its few
+    // split blocks a join.)
     bool split = true;
     if (threads == 32) {
         int all = sub == 0 ? blocks : 0;

@@ -1,6 +1,6 @@
 // attn_tc.cuh -- pieces shared by the two tensor-core attention kernels: 8-bit
-// tcgen05 products, the page-by-page tile copies of the cache, and the cut of a
-// ragged batch into equal shares.
+// tcgen05 products, the split of q and of weights into two e4m3 numbers, the score
+// cap, bounded waits and the page-by-page tile copies of the cache.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -110,9 +110,9 @@ __device__ __forceinline__ float redux_max(float x)
     return y;
 }
 
-// Two e4m3 numbers whose sum is (x, y), each below 2^15, to within 2^-8 of each and 2^-10: the low byte of each
-// result is x's. By way of fp16, which both conversions and the difference between them take two at a time; its
-// rounding, 2^-11, is an eighth of the sum's.
+// Two e4m3 numbers whose sum is (x, y), to within 2^-8 of each and 2^-10, for magnitudes up to 448 (callers stay at 256
+// and below): the low byte of each result is x's. By way of fp16, which both conversions and the difference between
+// them take two at a time; its rounding, 2^-11, is an eighth of the sum's.
 __device__ __forceinline__ void split_e4m3(float x, float y, uint32_t &hi, uint32_t &lo)
 {
     const __half2 v = __floats2half2_rn(x, y);

@@ -552,13 +552,14 @@ size_t gdn_attn_workspace_bytes(const gdn_attn_dims *dims, int32_t prefill);
  *        16-byte aligned; contents on entry do not matter. Calls that overlap
  *        on the GPU need separate workspaces.
  * Scores, statistics and sums are float32. Keys and values enter the products
- * as they are held. q enters as two e4m3 numbers, exact down to 2^-18 of the
- * row's largest element; a weight is rounded to 2^-8 of itself (two e4m3
- * numbers, bf16 in gdn_attn_prefill) before it meets v, not in the sum.
- * RANGE of values, whatever the scores: sums of 2^17 keys hold in
- * gdn_attn_decode, for v_scales of 2^-75 or more within 2^70 of one another, and for
- * pages of zeros beside v_scales up to 1; in gdn_attn_prefill, for a v_scale of 2^-50 or more, while the largest held
- * value times the number of keys is below 2^70 (2^45 with a softcap up to 55).
+ * as they are held. q enters as two e4m3 numbers, exact down to 2^-17 of the
+ * row's largest element (or 2^-136); a weight is rounded to 2^-8 of itself (two
+ * e4m3 numbers, bf16 in gdn_attn_prefill) before it meets v, not in the sum.
+ * RANGE of values, whatever the scores: sums of 2^17 keys hold
+ *   in gdn_attn_decode for v_scales of 2^-75 or more within 2^70 of one another,
+ *     and for pages of zeros beside v_scales up to 1;
+ *   in gdn_attn_prefill for v_scales of 2^-50 or more, while the largest held value
+ *     times the number of keys is below 2^70 (2^45 with a softcap up to 55).
  * Beyond that an output may come out as zero or infinite.
  * Two launches: the second joins rows whose keys were shared out.
  * Errors: INVALID_ARG (null, sizes, alignment, scale or softcap not finite,
