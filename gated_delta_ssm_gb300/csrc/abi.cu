@@ -752,7 +752,10 @@ void gdn_testing_row_splits(int32_t n_seq, int32_t n_v_heads, int32_t r, int32_t
 gdn_status gdn_check_device(int32_t *code)
 {
     int a = 0, b = 0, c = 0, d = 0, e = 0, f = 0, g = 0;
-    gdn_status st = from_cuda(gdn::take_decode_device_error(&a));
+    // the copies below wait for the default stream alone, not for streams that do not wait for it either
+    gdn_status st = from_cuda(cudaDeviceSynchronize());
+    if (st == GDN_OK)
+        st = from_cuda(gdn::take_decode_device_error(&a));
     if (st == GDN_OK)
         st = from_cuda(gdn::take_prefill_device_error(&b));
     if (st == GDN_OK)
